@@ -239,9 +239,12 @@ def run(state):
                                      s["status"], s["out"], s["workspace"], softcap=s["cap"], window=s["window"],
                                      alibi_slopes=s["slopes"], slot=s["slot"])
             return s["out"]
+        if "workspace" not in s:
+            s["workspace"] = tv.accept_sample_workspace(s["B"], s["M"], s["V"], s["logits"].device)
         tv.tree_accept_sample(s["logits"], s["uniform"], s["temperature"], s["draft"], s["parent"], s["depth"],
                               s["anc_words"], s["status"], s["max_depth"], s["token"], s["accept_len"], s["path"],
-                              s["bonus"], top_k=s["top_k"], top_p=s["top_p"], min_p=s["min_p"], logprob=s["logprob"])
+                              s["bonus"], s["workspace"], top_k=s["top_k"], top_p=s["top_p"], min_p=s["min_p"],
+                              logprob=s["logprob"])
         return s["token"], s["logprob"], s["accept_len"], s["path"], s["bonus"]
     return {"norm_rope": _norm_rope, "attention": _attention, "sample": _sample}[s["op"]](s)
 
