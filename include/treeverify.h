@@ -206,6 +206,38 @@ tv_status tree_attention_noalloc(const uint16_t* q, const uint16_t* k, const uin
                                  uint16_t* out, tv_stream_t stream);
 
 /*
+ * tree_attention_scored -- tree_attention for teachers whose scores are capped,
+ * local or biased by distance.  With pos(u) = kv_len[b] + depth[b][u] for tree
+ * row u and pos(j) = j for prefix column j, the score of query row u, head h
+ * and key x is
+ *   s = scale * q.k
+ *   s = softcap * tanh(s / softcap)                 if softcap > 0
+ *   s = s - alibi_slopes[h] * (pos(u) - pos(x))     if alibi_slopes is given
+ * and the key takes part iff tree_attention would let it and, with window > 0,
+ * pos(u) - pos(x) < window.
+ *
+ *   softcap >= 0; window >= 0 (0: no window); alibi_slopes fp32 [Hq] in or NULL
+ *   depth     int32 [B][M+1] in (from tree_build_mask); may be NULL without a
+ *             window and without slopes
+ *   workspace device scratch of tree_attention_scored_workspace_size(...) bytes,
+ *             as for tree_attention: no initialisation, dead after the call, not
+ *             shared by calls (or captured graphs) that overlap on the device
+ *   everything else as for tree_attention, head dims 64 and 128 alike; a row
+ *   without a key gets zeros.
+ * Contract: the K/V rows that some query row of the sequence may read hold
+ * finite values; prefix columns before the root's window are not used, whatever
+ * they hold.
+ */
+size_t tree_attention_scored_workspace_size(int B, int M, int Hq, int Hkv, int D, int64_t S_cap, int window);
+
+tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t S_cap,
+                                const int32_t* kv_start, const int32_t* kv_len, const uint32_t* anc_mask,
+                                const int32_t* depth, int32_t* status, int B, int M, int Hq, int Hkv, int D,
+                                float scale, float softcap, int window, const float* alibi_slopes, uint16_t* out,
+                                void* workspace, size_t workspace_bytes, const int32_t* slot, int n_slots,
+                                tv_stream_t stream);
+
+/*
  * tree_accept -- per-node greedy argmax of the teacher logits fused with
  * longest accepted path selection.  [EAGLE-Pangu, results: accepted length per
  * verification step.]  Node i is accepted iff its parent is accepted and
@@ -255,6 +287,60 @@ tv_status tree_accept_lm_head(const uint16_t* hidden, const uint16_t* w_lm, cons
                               int32_t* status, int B, int M, int H, int V, int max_depth, int32_t* argmax,
                               int32_t* accept_len, int32_t* path, int32_t* bonus, void* workspace,
                               size_t workspace_bytes, tv_stream_t stream);
+
+/*
+ * tree_accept_sample -- tree_accept for a teacher that samples: each node's
+ * next token is drawn from the teacher's filtered distribution with a given
+ * random number, and the acceptance walk runs on the drawn tokens.  A node is
+ * accepted iff its parent is and its draft is the token drawn at its parent, so
+ * every token that leaves the step is a draw of the teacher itself.
+ *
+ * For a row with logits l, m = max l and T = temperature[b], the tokens in the
+ * order (l descending, index ascending) have the weights w = exp((l - m) / T).
+ * Kept is a prefix of that order:
+ *   top-k   the first top_k[b] tokens (off for top_k <= 0 or >= V)
+ *   top-p   of these, each token while the weight before it is below top_p[b]
+ *           times the weight of all of them (off for top_p >= 1)
+ *   min-p   of these, each token with w >= min_p[b] (off for min_p <= 0)
+ * and always the first token.  Drawn is the first kept token in vocabulary
+ * order whose inclusive sum of kept weights exceeds uniform[b][u] times the sum
+ * of all kept weights (the last kept one if none does).  T <= 0 draws the first
+ * token of the order (greedy).  A setting that is NaN counts as off (greedy for
+ * the temperature).
+ *
+ *   logits     fp32 or bf16 [B][M+1][V], rows logits_stride elements apart
+ *              (logits_stride >= V; no alignment beyond the type's own)
+ *   logits_type  TV_LOGITS_F32 or TV_LOGITS_BF16.  A logit of -inf or NaN is
+ *              never drawn; with logits of +inf the draw is uniform over those.
+ *   uniform    fp32 [B][M+1] in, random numbers in [0, 1)
+ *   temperature  fp32 [B] in; top_k int32 [B], top_p, min_p fp32 [B] in, each may
+ *              be NULL (off)
+ *   draft, parent, depth, anc_mask, status, accept_len, path, bonus: as for
+ *              tree_accept
+ *   token      int32 [B][M+1]  out: the token drawn at every node; -1 for a row
+ *              without a logit above -inf.  Such a row matches no draft, and a
+ *              sequence whose path would end there is rejected (accept_len = -1,
+ *              status unchanged)
+ *   logprob    fp32 [B][M+1] out, may be NULL: log of the drawn token's
+ *              probability among the kept tokens (-inf where token = -1)
+ *   1 <= V <= 262144 (TV_ERR_UNSUPPORTED above).
+ *   workspace  device scratch of tree_accept_sample_workspace_size(...) bytes, 16-byte
+ *              aligned: no initialisation, dead after the call, not shared by
+ *              calls (or captured graphs) that overlap on the device
+ * A row's token depends on its logits, its random number and its settings only,
+ * not on the batch, the launch or the device's other work.
+ */
+#define TV_LOGITS_F32 0
+#define TV_LOGITS_BF16 1
+
+size_t tree_accept_sample_workspace_size(int B, int M, int V);
+
+tv_status tree_accept_sample(const void* logits, int logits_type, int64_t logits_stride, const float* uniform,
+                             const float* temperature, const int32_t* top_k, const float* top_p,
+                             const float* min_p, const int32_t* draft, const int32_t* parent,
+                             const int32_t* depth, const uint32_t* anc_mask, int32_t* status, int B, int M, int V,
+                             int max_depth, int32_t* token, float* logprob, int32_t* accept_len, int32_t* path,
+                             int32_t* bonus, void* workspace, size_t workspace_bytes, tv_stream_t stream);
 
 /*
  * kv_commit_realign -- commit the accepted path into the KV cache of every
@@ -319,6 +405,41 @@ tv_status tree_kv_write(uint16_t* const* k_layers, uint16_t* const* v_layers, co
                         const uint16_t* tree_v, int L, int B, int Hkv, int D, int64_t S_cap, int M,
                         const int32_t* kv_start, const int32_t* kv_len, const int32_t* depth, float rope_theta,
                         const int32_t* slot, int n_slots, tv_stream_t stream);
+
+/*
+ * tree_qk_norm_rope -- from the packed projection rows of one layer to
+ * attention-ready queries and cache rows in one pass, for teachers that
+ * normalise every query and key head: RMS norm over each head, its weight, the
+ * rotation to the tree position kv_len[b] + depth[b][u] (as TV_ATTN_ROPE and
+ * tree_kv_write rotate; half-split pairs), and the append of the K and V rows
+ * behind the committed prefix (as tree_kv_write places them).
+ *
+ *   qkv       bf16 [B][M+1][(Hq + 2 Hkv) * D] in: query heads, key heads, value
+ *             heads of every tree node; rows qkv_stride elements apart
+ *             (qkv_stride >= (Hq + 2 Hkv) * D, a multiple of 8)
+ *   q_weight, k_weight  bf16 [D] in, each may be NULL (no weight): element d of
+ *             a normalised head is scaled by weight_offset + weight[d]
+ *             (weight_offset = 0, or 1 for weights stored around zero)
+ *   eps >= 0  y = x / sqrt(mean(x^2) + eps)
+ *   q_out     bf16 [B][M+1][Hq][D] out
+ *   k, v      bf16 [B][Hkv][S_cap][D] (one layer), written at columns kv_start[b]
+ *             + kv_len[b] + r, r = 0..M; every other cell is left as it was
+ *   depth     int32 [B][M+1] in (from tree_build_mask)
+ *   rotary_dim  leading elements of each head that are rotated, a multiple of 16
+ *             up to D (0: none); pair (i, i + rotary_dim/2), i < rotary_dim/2,
+ *             turns by position * rope_theta^(-2i/rotary_dim); rope_theta > 1
+ *   slot, n_slots  optional slot map (see tree_attention)
+ *   D in {64, 128}; 0 <= M < 256; qkv, q_weight, k_weight, q_out, k, v 16-byte
+ *   aligned.
+ * All arithmetic is fp32 (angles double), rounded once to bf16; V rows are
+ * copied as they are.  A sequence with a bad geometry or slot is left
+ * untouched, its q_out rows too (tree_attention_scored gives it zero rows).
+ */
+tv_status tree_qk_norm_rope(const uint16_t* qkv, int64_t qkv_stride, const uint16_t* q_weight,
+                            const uint16_t* k_weight, float weight_offset, float eps, uint16_t* q_out, uint16_t* k,
+                            uint16_t* v, int64_t S_cap, const int32_t* kv_start, const int32_t* kv_len,
+                            const int32_t* depth, int B, int M, int Hq, int Hkv, int D, int rotary_dim,
+                            float rope_theta, const int32_t* slot, int n_slots, tv_stream_t stream);
 
 /* Human-readable name of a tv_status. */
 const char* tv_status_string(tv_status s);

@@ -379,3 +379,162 @@ def argmax_rows_f64(x):
     out = np.zeros((x.size // V,), np.int32)
     lib().oracle_argmax_rows_f64(_p(x), x.size // V, V, _p(out))
     return out.reshape(x.shape[:-1])
+
+
+# ----------------------------------------------------------------------------- per-head norms, scored attention, sampling
+# Plain float64 readings of the operators for teachers with normalised query and
+# key heads, capped / local / distance-biased scores and sampled decoding.  The
+# tree is walked through the parent pointers, as above.
+
+def bf16_to_f64(bits):
+    """The float64 values of bf16 bit patterns."""
+    return (_bits16(bits).astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+
+
+def _geometry_ok(ks, kl, n, S_cap):
+    return ks >= 0 and kl >= 0 and int(ks) + int(kl) + n <= S_cap
+
+
+def tree_qk_norm_rope(qkv, q_weight, k_weight, weight_offset, eps, k, v, kv_start, kv_len, depth, Hq, Hkv,
+                      rotary_dim, theta, slots=None):
+    """qkv bf16-bits [B][n][Hq + 2 Hkv][D] -> (q, k, v) as float64: q [B][n][Hq][D], and copies of the caches
+    k, v (bf16-bits [n_slots][Hkv][S_cap][D]) with the step's rows written.  q rows of a sequence whose geometry or
+    slot is bad are NaN (left untouched by the call).  Also returns, for q and the k rows, |a| + |b| of each
+    element's rotated pair (its own magnitude where nothing rotates): the scale of the rotation's rounding errors."""
+    x = bf16_to_f64(qkv)
+    B, n, heads, D = x.shape
+    assert heads == Hq + 2 * Hkv
+    q = np.full((B, n, Hq, D), np.nan)
+    kc, vc = bf16_to_f64(k), bf16_to_f64(v)
+    qmag, kmag = np.zeros_like(q), np.zeros_like(kc)
+    S_cap = kc.shape[2]
+    half = rotary_dim // 2
+    for b in range(B):
+        sl = b if slots is None else int(slots[b])
+        if not 0 <= sl < kc.shape[0] or not _geometry_ok(kv_start[sl], kv_len[sl], n, S_cap):
+            continue
+        for u in range(n):
+            pos = int(kv_len[sl]) + int(depth[b][u])
+            col = int(kv_start[sl]) + int(kv_len[sl]) + u
+            for h in range(heads):
+                y = x[b, u, h]
+                if h >= Hq + Hkv:
+                    vc[sl, h - Hq - Hkv, col] = y
+                    continue
+                w = q_weight if h < Hq else k_weight
+                scale = 1.0 if w is None else weight_offset + bf16_to_f64(w)
+                y = y / math.sqrt(float(np.mean(y * y)) + eps) * scale
+                z, mag = y.copy(), np.abs(y)
+                for i in range(half):
+                    t = pos * theta ** (-2.0 * i / rotary_dim)
+                    z[i] = y[i] * math.cos(t) - y[i + half] * math.sin(t)
+                    z[i + half] = y[i + half] * math.cos(t) + y[i] * math.sin(t)
+                    mag[i] = mag[i + half] = abs(y[i]) + abs(y[i + half])
+                if h < Hq:
+                    q[b, u, h], qmag[b, u, h] = z, mag
+                else:
+                    kc[sl, h - Hq, col], kmag[sl, h - Hq, col] = z, mag
+    return q, kc, vc, qmag, kmag
+
+
+def tree_attention_scored(q, k, v, kv_start, kv_len, parent, status, Hkv: int, scale=None, softcap=0.0, window=0,
+                          slopes=None, slots=None):
+    """-> (out, mean) float64 [B][n][Hq][D]: softmax(scores) v over each node's keys, and the same weights over |v|
+    (the scale of the rounding errors of the weights).  Rows without a key are zero."""
+    qf, kf, vf = bf16_to_f64(q), bf16_to_f64(k), bf16_to_f64(v)
+    B, n, Hq, D = qf.shape
+    S_cap = kf.shape[2]
+    G = Hq // Hkv
+    scale = D ** -0.5 if scale is None else scale
+    out, mean = np.zeros_like(qf), np.zeros_like(qf)
+    for b in range(B):
+        sl = b if slots is None else int(slots[b])
+        if status[b] != 0 or not 0 <= sl < kf.shape[0] or not _geometry_ok(kv_start[sl], kv_len[sl], n, S_cap):
+            continue
+        L, c0 = int(kv_len[sl]), int(kv_start[sl])
+        dep = np.zeros(n, np.int64)
+        for u in range(1, n):
+            dep[u] = dep[parent[b][u]] + 1
+        for u in range(n):
+            own, r = [], u
+            while True:
+                own.append(r)
+                if r == 0:
+                    break
+                r = int(parent[b][r])
+            keys = np.concatenate([np.arange(L), L + np.array(own[::-1], np.int64)])
+            dist = L + dep[u] - np.concatenate([np.arange(L), L + dep[own[::-1]]])
+            if window > 0:
+                keys, dist = keys[dist < window], dist[dist < window]
+            for h in range(Hq):
+                s = scale * (kf[sl, h // G, c0 + keys] @ qf[b, u, h])
+                if softcap > 0:
+                    s = softcap * np.tanh(s / softcap)
+                if slopes is not None:
+                    s = s - float(slopes[h]) * dist
+                p = np.exp(s - s.max())
+                p /= p.sum()
+                out[b, u, h] = p @ vf[sl, h // G, c0 + keys]
+                mean[b, u, h] = p @ np.abs(vf[sl, h // G, c0 + keys])
+    return out, mean
+
+
+def sample_row(logits, u, T=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """(token, log probability among the kept tokens, kept tokens in order) of one row."""
+    l = np.asarray(logits, np.float64)
+    l = np.where(np.isnan(l), -np.inf, l) + 0.0
+    order = [int(i) for i in np.argsort(-l, kind="stable") if l[i] > -np.inf]
+    if not order:
+        return -1, -np.inf, []
+    if not T > 0:
+        return order[0], 0.0, order[:1]
+    m = l[order[0]]
+    with np.errstate(invalid="ignore"):
+        w = {i: 1.0 if l[i] == m else math.exp((l[i] - m) / T) for i in order}
+    if top_k > 0:
+        order = order[:top_k]
+    total, before, kept = math.fsum(w[i] for i in order), 0.0, []
+    for i in order:
+        if kept and ((top_p < 1 and not before < top_p * total) or (min_p > 0 and not w[i] >= min_p)):
+            break
+        kept.append(i)
+        before = math.fsum([before, w[i]])
+    S = math.fsum(w[i] for i in kept)
+    token, cum = None, 0.0
+    for i in sorted(kept):
+        cum += w[i]
+        if cum > u * S:
+            token = i
+            break
+    if token is None:
+        token = max(i for i in kept if w[i] > 0)
+    return token, math.log(w[token]) - math.log(S), kept
+
+
+def tree_accept_sample(logits, uniform, temperature, draft, parent, status, max_depth, top_k=None, top_p=None,
+                       min_p=None):
+    """-> (token [B][n], logprob [B][n], accept_len, path, bonus): sample_row at every node, then the longest
+    root-to-node path whose drafts are the tokens drawn at their parents (lowest row on ties)."""
+    B, n, _ = logits.shape
+    token, logprob = np.zeros((B, n), np.int32), np.zeros((B, n))
+    alen, path, bonus = np.full(B, -1, np.int32), np.zeros((B, max_depth + 1), np.int32), np.zeros(B, np.int32)
+    for b in range(B):
+        for u in range(n):
+            token[b, u], logprob[b, u], _ = sample_row(
+                logits[b, u], float(uniform[b, u]), float(temperature[b]), 0 if top_k is None else int(top_k[b]),
+                1.0 if top_p is None else float(top_p[b]), 0.0 if min_p is None else float(min_p[b]))
+        if status[b] != 0:
+            continue
+        best = [0]
+        for u in range(n):
+            r, p = u, [u]
+            while r != 0 and draft[b][r] == token[b, parent[b][r]] and token[b, parent[b][r]] >= 0:
+                r = int(parent[b][r])
+                p.append(r)
+            if r == 0 and len(p) > len(best):
+                best = p[::-1]
+        if token[b, best[-1]] < 0:
+            continue
+        alen[b], bonus[b] = len(best) - 1, token[b, best[-1]]
+        path[b, :len(best)] = best
+    return token, logprob, alen, path, bonus

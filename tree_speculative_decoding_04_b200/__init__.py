@@ -17,6 +17,8 @@ from ._lib import (  # noqa: F401
     SEQ_TIMEOUT,
     SEQ_TOO_DEEP,
     TVError,
+    accept_sample_workspace,
+    attention_scored_workspace,
     attention_workspace,
     kv_commit_realign,
     layer_pointers,
@@ -24,9 +26,12 @@ from ._lib import (  # noqa: F401
     set_wait_limit_ns,
     tree_accept,
     tree_accept_lm_head,
+    tree_accept_sample,
     lm_head_workspace,
     tree_attention,
+    tree_attention_scored,
     tree_attention_workspace_size,
     tree_build_mask,
     tree_kv_write,
+    tree_qk_norm_rope,
 )

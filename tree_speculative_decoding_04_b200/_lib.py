@@ -30,11 +30,16 @@ EXPORTS = (
     "tree_attention",
     "tree_attention_noalloc_max_scratch",
     "tree_attention_noalloc",
+    "tree_attention_scored_workspace_size",
+    "tree_attention_scored",
     "tree_accept",
     "tree_accept_lm_head_workspace_size",
     "tree_accept_lm_head",
+    "tree_accept_sample_workspace_size",
+    "tree_accept_sample",
     "kv_commit_realign",
     "tree_kv_write",
+    "tree_qk_norm_rope",
     "tv_status_string",
     "tv_last_cuda_error",
     "tv_version",
@@ -74,8 +79,18 @@ def load(path: str = LIB_PATH):
                                         P]
     lib.kv_commit_realign.argtypes = [P, P, i32, i32, i32, i32, i64, i32, P, P, P, i32, P, P, P, i32, P, P, P, i32, P]
     lib.tree_kv_write.argtypes = [P, P, P, P, i32, i32, i32, i32, i64, i32, P, P, P, f32, P, i32, P]
+    lib.tree_attention_scored_workspace_size.argtypes = [i32, i32, i32, i32, i32, i64, i32]
+    lib.tree_attention_scored_workspace_size.restype = ctypes.c_size_t
+    lib.tree_attention_scored.argtypes = [P, P, P, i64, P, P, P, P, P, i32, i32, i32, i32, i32, f32, f32, i32, P, P,
+                                          P, ctypes.c_size_t, P, i32, P]
+    lib.tree_accept_sample_workspace_size.argtypes = [i32, i32, i32]
+    lib.tree_accept_sample_workspace_size.restype = ctypes.c_size_t
+    lib.tree_accept_sample.argtypes = [P, i32, i64, P, P, P, P, P, P, P, P, P, P, i32, i32, i32, i32, P, P, P, P, P,
+                                       P, ctypes.c_size_t, P]
+    lib.tree_qk_norm_rope.argtypes = [P, i64, P, P, f32, f32, P, P, P, i64, P, P, P, i32, i32, i32, i32, i32, i32,
+                                      f32, P, i32, P]
     for name in ("tree_build_mask", "tree_attention", "tree_accept", "tree_accept_lm_head", "kv_commit_realign",
-                 "tree_kv_write"):
+                 "tree_kv_write", "tree_attention_scored", "tree_accept_sample", "tree_qk_norm_rope"):
         getattr(lib, name).restype = ctypes.c_int
     lib.tv_status_string.argtypes = [ctypes.c_int]
     lib.tv_status_string.restype = ctypes.c_char_p
@@ -110,6 +125,59 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+class _on:
+    """The device of the tensors as the current one for a call, and the call's
+    stream (the given one, else that device's current one) as its pointer.  All
+    tensors must live on that one GPU."""
+
+    __slots__ = ("dev", "stream", "back")
+
+    def __init__(self, stream, *tensors):
+        self.dev, self.stream, self.back = tensors[0].get_device(), stream, -1
+        for t in tensors:
+            if t is not None and t.get_device() != self.dev:
+                raise TVError("tensors must live on one GPU")
+
+    def __enter__(self):
+        if self.dev < 0:
+            raise TVError("tensor must live on the GPU")
+        if torch.cuda.current_device() != self.dev:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.dev)
+        if self.stream is None:
+            return ctypes.c_void_p(torch.cuda.current_stream(self.dev).cuda_stream)
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.back >= 0:
+            torch.cuda.set_device(self.back)
+        return False
+
+
+def _row_stride(t: torch.Tensor, width: int, name: str) -> int:
+    """Elements between the rows of t [B][M+1][...], each row `width` contiguous
+    elements and all rows evenly spaced (a dense tensor, or the leading columns of
+    one that is wider)."""
+    B, n = t.shape[0], t.shape[1]
+    inner, want = t.stride()[2:], 1
+    for size, st in zip(reversed(t.shape[2:]), reversed(inner)):
+        if size != 1 and st != want:
+            raise TVError(f"{name}: a row must be contiguous")
+        want *= size
+    if B * n <= 1:
+        return width
+    row = t.stride(1) if n > 1 else t.stride(0)
+    if row < width or (B > 1 and n > 1 and t.stride(0) != n * row):
+        raise TVError(f"{name}: rows must be evenly spaced")
+    return row
+
+
+def _ptr_rows(t: torch.Tensor):
+    if not t.is_cuda:
+        raise TVError("tensor must live on the GPU")
+    return ctypes.c_void_p(t.data_ptr())
 
 
 def _need(t: torch.Tensor, dtype, shape, name):
@@ -222,6 +290,134 @@ def tree_accept_lm_head(hidden, w_lm, draft, parent, depth, anc_mask, status, ma
                                     _ptr(status), B, n - 1, H, V, int(max_depth), _ptr(argmax), _ptr(accept_len),
                                     _ptr(path), _ptr(bonus), _ptr(workspace), ws_bytes, _stream(stream))
     _check(rc, "tree_accept_lm_head")
+
+
+def attention_scored_workspace(B, M, Hq, Hkv, D, S_cap, window, device) -> torch.Tensor | None:
+    """A device buffer of tree_attention_scored_workspace_size bytes for this shape
+    (None when no workspace is needed).  Calls that may overlap need one each."""
+    with torch.cuda.device(device):
+        nbytes = int(load().tree_attention_scored_workspace_size(B, M, Hq, Hkv, D, int(S_cap), int(window)))
+    if nbytes == 0:
+        return None
+    return torch.empty((nbytes + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def tree_attention_scored(q, k, v, kv_start, kv_len, anc_mask, depth, status, out, workspace=None, scale=None,
+                          softcap=0.0, window=0, alibi_slopes=None, stream=None, slot=None):
+    """tree_attention with capped, local or distance-biased scores.
+
+    q [B][M+1][Hq][D] bf16; k, v [B][Hkv][S_cap][D] bf16 (one layer; with slot a
+    pool [n_slots][Hkv][S_cap][D], kv_start / kv_len [n_slots]) -> out like q.
+    softcap: s -> softcap * tanh(s / softcap) (0: off).  window: only keys closer
+    than this many positions (0: off).  alibi_slopes fp32 [Hq]: s - slope *
+    distance.  workspace: attention_scored_workspace(...)."""
+    B, n, Hq, D = q.shape
+    Hkv, S_cap = k.shape[1], k.shape[2]
+    NS = k.shape[0] if slot is not None else B
+    _need(q, torch.bfloat16, (B, n, Hq, D), "q")
+    _need(k, torch.bfloat16, (NS, Hkv, S_cap, D), "k")
+    _need(v, torch.bfloat16, (NS, Hkv, S_cap, D), "v")
+    _need(kv_start, torch.int32, (NS,), "kv_start")
+    _need(kv_len, torch.int32, (NS,), "kv_len")
+    _need(anc_mask, torch.int32, (B, n, (n + 31) // 32), "anc_mask")
+    _need(depth, torch.int32, (B, n), "depth")
+    _need(status, torch.int32, (B,), "status")
+    _need(out, torch.bfloat16, (B, n, Hq, D), "out")
+    if slot is not None:
+        _need(slot, torch.int32, (B,), "slot")
+    if alibi_slopes is not None:
+        _need(alibi_slopes, torch.float32, (Hq,), "alibi_slopes")
+    if scale is None:
+        scale = D ** -0.5
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on(stream, q, k, v, kv_start, kv_len, anc_mask, depth, status, out, workspace, alibi_slopes, slot) as s:
+        rc = load().tree_attention_scored(_ptr(q), _ptr(k), _ptr(v), S_cap, _ptr(kv_start), _ptr(kv_len),
+                                          _ptr(anc_mask), _ptr(depth), _ptr(status), B, n - 1, Hq, Hkv, D,
+                                          float(scale), float(softcap), int(window), _ptr(alibi_slopes), _ptr(out),
+                                          _ptr(workspace), ws_bytes, _ptr(slot), NS, s)
+    _check(rc, "tree_attention_scored")
+
+
+def accept_sample_workspace(B, M, V, device) -> torch.Tensor:
+    """A device buffer of tree_accept_sample_workspace_size bytes for this shape.
+    Calls that may overlap need one each."""
+    nbytes = int(load().tree_accept_sample_workspace_size(B, M, V))
+    return torch.empty((max(nbytes, 8) + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def tree_accept_sample(logits, uniform, temperature, draft, parent, depth, anc_mask, status, max_depth, token,
+                       accept_len, path, bonus, workspace, top_k=None, top_p=None, min_p=None, logprob=None,
+                       stream=None):
+    """tree_accept with a token drawn at every node instead of the argmax.
+
+    logits fp32 or bf16 [B][M+1][V] (evenly spaced rows, such as the first V
+    columns of a padded vocabulary); uniform fp32 [B][M+1]; temperature fp32 [B]
+    (<= 0: greedy); top_k int32 [B], top_p / min_p fp32 [B] or None (off).  Writes
+    token int32 [B][M+1], logprob fp32 [B][M+1] (optional), accept_len, path and
+    bonus.  workspace: accept_sample_workspace(...)."""
+    B, n, V = logits.shape
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TVError(f"logits: dtype {logits.dtype}, expected torch.float32 or torch.bfloat16")
+    stride = _row_stride(logits, V, "logits")
+    for t, name in ((uniform, "uniform"), (logprob, "logprob")):
+        if t is not None or name == "uniform":
+            _need(t, torch.float32, (B, n), name)
+    for t, name in ((draft, "draft"), (parent, "parent"), (depth, "depth"), (token, "token")):
+        _need(t, torch.int32, (B, n), name)
+    _need(temperature, torch.float32, (B,), "temperature")
+    if top_k is not None:
+        _need(top_k, torch.int32, (B,), "top_k")
+    for t, name in ((top_p, "top_p"), (min_p, "min_p")):
+        if t is not None:
+            _need(t, torch.float32, (B,), name)
+    _need(anc_mask, torch.int32, (B, n, (n + 31) // 32), "anc_mask")
+    _need(status, torch.int32, (B,), "status")
+    _need(accept_len, torch.int32, (B,), "accept_len")
+    _need(path, torch.int32, (B, int(max_depth) + 1), "path")
+    _need(bonus, torch.int32, (B,), "bonus")
+    with _on(stream, logits, uniform, temperature, draft, parent, depth, anc_mask, status, token, accept_len, path,
+             bonus, workspace, top_k, top_p, min_p, logprob) as s:
+        rc = load().tree_accept_sample(_ptr_rows(logits), int(logits.dtype == torch.bfloat16), stride, _ptr(uniform),
+                                       _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(draft),
+                                       _ptr(parent), _ptr(depth), _ptr(anc_mask), _ptr(status), B, n - 1, V,
+                                       int(max_depth), _ptr(token), _ptr(logprob), _ptr(accept_len), _ptr(path),
+                                       _ptr(bonus), _ptr(workspace), workspace.numel() * workspace.element_size(), s)
+    _check(rc, "tree_accept_sample")
+
+
+def tree_qk_norm_rope(qkv, q_weight, k_weight, q_out, k, v, kv_start, kv_len, depth, eps=1e-6, weight_offset=0.0,
+                      rope_theta=10000.0, rotary_dim=None, stream=None, slot=None):
+    """The packed projection rows of one layer -> queries and cache rows.
+
+    qkv bf16 [B][M+1][Hq + 2 Hkv][D] (evenly spaced rows): every query and key head
+    is RMS-normalised, scaled by weight_offset + its weight (bf16 [D], None: no
+    weight) and rotated to kv_len + depth over its first rotary_dim elements
+    (default D, 0: no rotation); q goes to q_out [B][M+1][Hq][D], k and v rows to
+    columns kv_start + kv_len + r of the layer's cache k, v [B][Hkv][S_cap][D] (a
+    pool [n_slots][Hkv][S_cap][D] with slot)."""
+    B, n, Hq, D = q_out.shape
+    Hkv, S_cap = k.shape[1], k.shape[2]
+    NS = k.shape[0] if slot is not None else B
+    heads = Hq + 2 * Hkv
+    _need(qkv, torch.bfloat16, (B, n, heads, D), "qkv")
+    stride = _row_stride(qkv, heads * D, "qkv")
+    _need(q_out, torch.bfloat16, (B, n, Hq, D), "q_out")
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _need(t, torch.bfloat16, (D,), name)
+    _need(k, torch.bfloat16, (NS, Hkv, S_cap, D), "k")
+    _need(v, torch.bfloat16, (NS, Hkv, S_cap, D), "v")
+    _need(kv_start, torch.int32, (NS,), "kv_start")
+    _need(kv_len, torch.int32, (NS,), "kv_len")
+    _need(depth, torch.int32, (B, n), "depth")
+    if slot is not None:
+        _need(slot, torch.int32, (B,), "slot")
+    with _on(stream, q_out, qkv, q_weight, k_weight, k, v, kv_start, kv_len, depth, slot) as s:
+        rc = load().tree_qk_norm_rope(_ptr_rows(qkv), stride, _ptr(q_weight), _ptr(k_weight), float(weight_offset),
+                                      float(eps), _ptr(q_out), _ptr(k), _ptr(v), S_cap, _ptr(kv_start), _ptr(kv_len),
+                                      _ptr(depth), B, n - 1, Hq, Hkv, D, D if rotary_dim is None else int(rotary_dim),
+                                      float(rope_theta), _ptr(slot), NS, s)
+    _check(rc, "tree_qk_norm_rope")
 
 
 def kv_commit_realign(k_layer_ptrs, v_layer_ptrs, B, Hkv, D, S_cap, M, path, accept_len, status, max_depth,

@@ -168,7 +168,9 @@ __global__ void __launch_bounds__(kMaxRows) accept_walk_kernel(
     }
     return;
   }
-  const bool ok = in && (u == 0 || dr == argmax[rbase + p]);
+  // (a negative entry, a row without a token to choose, matches no draft)
+  const int tk = in ? argmax[rbase + p] : 0;
+  const bool ok = in && (u == 0 || (dr == tk && tk >= 0));
   const uint32_t ballot = __ballot_sync(0xffffffffu, ok);
   if ((u & 31) == 0) ok_bits[u >> 5] = ballot;
   __syncthreads();
@@ -194,13 +196,22 @@ __global__ void __launch_bounds__(kMaxRows) accept_walk_kernel(
   const int best = red[0];  // the root is always accepted, so best >= 0
   const int e = 0xffff - (best & 0xffff);
   const int de = best >> 16;
+  const int last = argmax[rbase + e];
+  if (last < 0) {  // no token follows the endpoint: the sequence is rejected
+    for (int j = u; j <= max_depth; j += blockDim.x) pth[j] = 0;
+    if (u == 0) {
+      accept_len[b] = -1;
+      bonus[b] = 0;
+    }
+    return;
+  }
   if (u < W) e_row[u] = anc[(rbase + e) * W + u];
   __syncthreads();
   if (in && ((e_row[u >> 5] >> (u & 31)) & 1u)) pth[dp] = u;
   for (int j = de + 1 + u; j <= max_depth; j += blockDim.x) pth[j] = 0;
   if (u == 0) {
     accept_len[b] = de;
-    bonus[b] = argmax[rbase + e];
+    bonus[b] = last;
   }
 }
 
