@@ -7,77 +7,835 @@
 // depth(u), prefix column j at position j, so distances inside the tree are
 // differences of depth.
 //
-// One warp per query row; an online softmax over the keys of the row.
+// For a query row (node u, head h) and a key x, in the log2 domain:
+//   s  = scale log2e (q.k)                          no cap
+//   s  = cap log2e tanh(scale (q.k) / cap)          cap
+//   s -= slope_h log2e (pos(u) - pos(x))            bias
+//   out = sum_x 2^(s - r) v_x / sum_x 2^(s - r)     for any reference r
+//
+// Work.  The G (M+1) query rows of a (sequence, kv head) form tiles of 128, the
+// keys it can see (from the root's window on) tiles of 128.  A CTA takes an
+// item: two query tiles and a range of key tiles.  Each of its two pipes (a
+// softmax warpgroup with a TMEM block of its own) owns one query tile and both
+// read every K/V tile; where only one query tile is left, the pipes share it
+// and take the even and the odd key tiles.  While one pipe's softmax runs, the
+// tensor core works for the other.
+//
+// Warps (384 threads, one CTA per SM): 0 requests K tiles, 2 V tiles, both into
+// one ring of slots in the order the MMAs use them; 1 issues the MMAs
+//   S_q  = Q K^T    M = 128, N = 128, A and B from shared memory -> TMEM
+//   O_q += P_q V    M = 128, N = D,   A = P from TMEM, V from shared memory
+// 4-7 and 8-11 are the pipes' softmax warps: thread t owns TMEM lane t, one
+// query row, and writes P over its scores.  QK_q of the next tile is issued
+// behind PV_q of this one, so a full S_q also says that PV_q is done.
 #include <algorithm>
+#include <climits>
 
-#include "tv_common.cuh"
+#include "attention_common.cuh"
+#include "tcgen05.cuh"
 
 namespace tv {
 namespace {
 
+constexpr int kQRows = 128;
+constexpr int kKeys = 128;                 // keys per tile
+constexpr int kHalf = kKeys * 128;         // one 64-column half of a tile: 128 rows x 128 B
+constexpr int kRingBytes = 163840;
+constexpr int kMaxSlots = 10;
+constexpr int kThreads = 384;
+constexpr float kGrow = 8.0f;              // the running maximum follows in steps of more than 2^8
+constexpr int kMaxBatch = 16384;
+constexpr int kMinSplitTiles = 4;          // key tiles below which a range is not split further
+constexpr int kMaxRankedRows = kThreads;
+
+// Which scores an instance computes.
+//   kCapLow: capped with cap * log2e <= kLowCap: every exponent lies within that of
+//   a fixed reference, so no maximum is kept and O is never rescaled
+enum Mode { kPlain = 0, kCapLow = 1, kCapHigh = 2, kBias = 3, kCapBias = 4 };
+constexpr float kLowCap = 85.f;
+
+// tanh(z) / z for |z| <= kPolyLim as a polynomial in z^2 (least relative error on
+// that range, found by iteratively reweighted least squares at Chebyshev nodes:
+// 5.7e-7), on the FMA pipe.  Beyond it tanh(z) = 1 - 2 / (e^2z + 1).
+constexpr double kPolyLim = 0.75;
+constexpr double kPoly[5] = {0.999999463558197, -0.3332825005054474, 0.13258983194828033, -0.050056301057338715,
+                             0.012929631397128105};
+
 struct ScoredParams {
-  const uint16_t *q, *k, *v;
+  const uint16_t* q;
   const int32_t *kv_start, *kv_len, *depth, *slot;
   const uint32_t* anc;
   int32_t* status;
   const float* slopes;
   uint16_t* out;
-  int64_t S_cap, rows;
-  int M, Hq, Hkv, G, W, n_slots, window;
-  float scale, cap;
+  int64_t S_cap;
+  int B, M, Hq, Hkv, G, W, n_slots, window;
+  int rows;         // G * (M + 1) query rows of a (sequence, kv head)
+  int nqt, npairs;  // query tiles, and items' pairs of them
+  int rec_rows;     // rows of a partial record
+  int sms;
+  int split;        // key ranges may be split over items
+  int cand_step;    // range lengths tried: kMinSplitTiles + i * cand_step tiles
+  float scale_log2, ref;
+  float c[5];       // capped score = x * (c0 + c1 x^2 + ...), x = q.k
+  float x_lim, z2, cap_log2;  // |x| of the polynomial's range; e^2z = 2^(z2 x); cap * log2e
+  uint64_t wait_limit_ns;
+  int* plan;        // [0]: key tiles per range, for the merge
+  float* ws_o;      // records [item][pipe][D / 4][rec_rows] float4
+  float2* ws_ml;    // [item][pipe][rec_rows] (reference, sum)
 };
 
-template <int D>
-__global__ void __launch_bounds__(128) scored_rows_kernel(const __grid_constant__ ScoredParams p) {
-  constexpr int E = D / 32;
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= p.rows) return;
-  const int n = p.M + 1;
-  const int h = (int)(row % p.Hq);
-  const int64_t node = row / p.Hq;
-  const int b = (int)(node / n);
-  const int sl = cache_slot(p.slot, b, p.n_slots);
-  const int32_t ks = sl >= 0 ? p.kv_start[sl] : -1, kl = sl >= 0 ? p.kv_len[sl] : 0;
-  float o[E], qv[E];
-  float m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  if (p.status[b] == 0 && geometry_ok(ks, kl, p.M, p.S_cap)) {
-    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q) + row * D + lane * E;
-    for (int e = 0; e < E; ++e) qv[e] = __bfloat162float(q[e]);
-    const int64_t base = (((int64_t)sl * p.Hkv + h / p.G) * p.S_cap + ks) * D + lane * E;
-    const __nv_bfloat16* K = reinterpret_cast<const __nv_bfloat16*>(p.k) + base;
-    const __nv_bfloat16* V = reinterpret_cast<const __nv_bfloat16*>(p.v) + base;
-    const int du = p.depth ? p.depth[node] : 0;
-    const float slope = p.slopes ? p.slopes[h] : 0.f;
-    const int first = p.window > 0 ? (int)max((int64_t)0, (int64_t)kl + du - p.window + 1) : 0;
-    for (int j = first; j < kl + n; ++j) {
-      int dist = kl + du - j;
-      if (j >= kl) {
-        const int r = j - kl;
-        if (!((p.anc[node * p.W + (r >> 5)] >> (r & 31)) & 1u)) continue;
-        dist = du - (p.depth ? p.depth[(int64_t)b * n + r] : 0);
-        if (p.window > 0 && dist >= p.window) continue;
+// A sequence's place in the cache, the first key that its root sees and the key
+// tiles from there (0: bad slot or geometry).  Its status has no part in this:
+// a call's CTAs and its merge form the plan at different times, and a sequence
+// may fail in between.
+struct Geo {
+  int sl, ks, kl, first, nt;
+};
+
+__device__ __forceinline__ Geo sequence(const ScoredParams& p, int b) {
+  Geo g{cache_slot(p.slot, b, p.n_slots), 0, 0, 0, 0};
+  if (g.sl < 0) return g;
+  g.ks = __ldcg(p.kv_start + g.sl);
+  g.kl = __ldcg(p.kv_len + g.sl);
+  if (!geometry_ok(g.ks, g.kl, p.M, p.S_cap)) return g;
+  if (p.window > 0) g.first = max(0, g.kl - (p.window - 1));
+  g.nt = (g.kl - g.first + p.M + 1 + kKeys - 1) / kKeys;
+  return g;
+}
+
+__device__ __forceinline__ int ranges_of(int nt, int len) { return nt <= len ? 1 : (nt + len - 1) / len; }
+
+struct Shared {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t drain;
+  unsigned long long best;
+  uint32_t tmem;
+  int timed_out;
+  int item_b, item_rem;
+  int alive;
+};
+
+// One capped score (log2) from the raw product x.
+__device__ __forceinline__ float cap_score(float x, const ScoredParams& p) {
+  const float t = x * x;
+  float g = p.c[4];
+#pragma unroll
+  for (int i = 3; i >= 0; --i) g = fmaf(g, t, p.c[i]);
+  return fabsf(x) <= p.x_lim ? x * g : p.cap_log2 * (1.f - __fdividef(2.f, fast_exp2(x * p.z2) + 1.f));
+}
+
+// 32 scores of a row, minus `sub`, from the raw products x of keys kc .. kc+31.
+// ok: the keys that count (used where `edge`).  slope2, pos: the row's bias per
+// position (log2) and its position.
+template <int MODE>
+__device__ __forceinline__ void chunk_scores(float (&x)[32], const ScoredParams& p, bool edge, uint32_t ok, float sub,
+                                             float slope2, int pos, int kc, int kl, int du, const int32_t* dep_b) {
+  constexpr bool CAP = MODE == kCapLow || MODE == kCapHigh || MODE == kCapBias;
+  constexpr bool BIAS = MODE == kBias || MODE == kCapBias;
+  if (edge) {  // rows behind the step's may hold anything
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (!((ok >> j) & 1u)) x[j] = 0.f;
+  }
+  const float base = BIAS ? -slope2 * (float)(pos - kc) - sub : -sub;
+  bool far = false;
+  if (CAP) {
+    float a[2] = {fabsf(x[0]), fabsf(x[1])};
+#pragma unroll
+    for (int j = 2; j < 32; j += 2) a[(j >> 1) & 1] = fmax3(a[(j >> 1) & 1], fabsf(x[j]), fabsf(x[j + 1]));
+    far = __any_sync(0xffffffffu, fmaxf(a[0], a[1]) > p.x_lim);
+  }
+  if (!far && !(BIAS && edge)) {
+    const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), b2 = f2_pack(base, base);
+    const uint64_t sl2 = f2_pack(slope2, slope2);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint64_t v = f2_pack(x[2 * j], x[2 * j + 1]);
+      uint64_t g = sc2;
+      if (CAP) {
+        const uint64_t t = f2_mul(v, v);
+        g = f2_pack(p.c[4], p.c[4]);
+#pragma unroll
+        for (int i = 3; i >= 0; --i) g = f2_fma(g, t, f2_pack(p.c[i], p.c[i]));
       }
-      float s = 0.f;
-      for (int e = 0; e < E; ++e) s += qv[e] * __bfloat162float(K[(int64_t)j * D + e]);
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      s *= p.scale;
-      if (p.cap > 0.f) s = p.cap * tanhf(s / p.cap);
-      s -= slope * (float)dist;
-      const float mn = fmaxf(m, s);
-      const float cr = m == -INFINITY ? 0.f : expf(m - mn), w = expf(s - mn);
-      l = l * cr + w;
-      for (int e = 0; e < E; ++e) o[e] = o[e] * cr + w * __bfloat162float(V[(int64_t)j * D + e]);
-      m = mn;
+      const uint64_t add = BIAS ? f2_fma(sl2, f2_pack((float)(2 * j), (float)(2 * j + 1)), b2) : b2;
+      f2_unpack(f2_fma(v, g, add), x[2 * j], x[2 * j + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float s = CAP ? cap_score(x[j], p) : x[j] * p.scale_log2;
+      float add = -sub;
+      if (BIAS) {
+        int dist = pos - (kc + j);
+        if (edge && kc + j >= kl) dist = du - (kc + j - kl <= p.M ? __ldg(dep_b + (kc + j - kl)) : 0);
+        add = fmaf(-slope2, (float)dist, -sub);
+      }
+      x[j] = s + add;
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + row * D + lane * E;
-  for (int e = 0; e < E; ++e) out[e] = __float2bfloat16_rn(o[e] * inv);
-  if (sl < 0 && lane == 0) atomicOr(&p.status[b], kSeqBadGeometry);
+  if (edge) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (!((ok >> j) & 1u)) x[j] = -INFINITY;
+  }
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    scored_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                  const __grid_constant__ ScoredParams p) {
+  constexpr bool BIAS = MODE == kBias || MODE == kCapBias;
+  constexpr bool TRACK = MODE != kCapLow;  // a running maximum is kept
+  constexpr int kHalves = D / 64;
+  constexpr int kTile = kHalves * kHalf;  // K, V or Q tile
+  constexpr int kSlots = kRingBytes / kTile;
+  static_assert(kSlots <= kMaxSlots, "ring");
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* q_s = smem;               // [2][halves][128][128 B]
+  uint8_t* ring = smem + 2 * kTile;  // [slots][halves][128][128 B]
+  Shared* sh = reinterpret_cast<Shared*>(ring + kRingBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    sh->timed_out = 0;
+    sh->best = ~0ull;
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], 1);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&sh->s_full[q], 1);
+      mbar_init(&sh->p_full[q], 4);
+      mbar_init(&sh->o_full[q], 1);
+    }
+    mbar_init(&sh->drain, 1);
+    fence_mbar_init();
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc(&sh->tmem, 512);
+    tmem_relinquish();
+  }
+  pdl_wait_primary();
+  pdl_launch_dependents();
+
+  // ---------------------------------------------------------------- which item
+  // Every CTA forms the same plan from the sequences' lengths: the number of key
+  // tiles per range that finishes first by this estimate (in steps of a pipe
+  // pair): rounds of items on the SMs x steps of an item, 3 steps of set-up and
+  // epilogue a round, 3 for the merge where ranges are split.  Each thread tries
+  // one length.
+  int* nt_s = reinterpret_cast<int*>(ring);
+  int* order = nt_s + p.B;
+  for (int b = tid; b < p.B; b += kThreads) nt_s[b] = sequence(p, b).nt;
+  __syncthreads();
+  int len = INT_MAX;
+  const int per_range = p.Hkv * p.npairs;  // items of one key range of a sequence
+  if (p.split) {
+    const int l = kMinSplitTiles + tid * p.cand_step;
+    // ceil(nt / l) by a reciprocal: exact while nt * 2^2 < 2^23, which the host's
+    // limit on split ranges ensures
+    const float inv = 1.f / (float)l, up = (float)l - 0.5f;
+    int64_t ranges = 0;
+    for (int b = 0; b < p.B; ++b) ranges += max(1, (int)(((float)nt_s[b] + up) * inv));
+    const int64_t items = ranges * per_range;
+    unsigned long long key = ~0ull;
+    if (items <= (int64_t)gridDim.x) {
+      const int64_t half_items = ranges * p.Hkv * p.nqt;  // a lone query tile takes half the steps
+      const int64_t rounds = p.nqt > 1 ? (half_items + 2 * p.sms - 1) / (2 * p.sms) : (items + p.sms - 1) / p.sms;
+      const int64_t steps = p.nqt > 1 ? l : (l + 1) / 2;
+      const int64_t est = rounds * steps + 3 * ((items + p.sms - 1) / p.sms) + (ranges > p.B ? 3 : 0);
+      key = (unsigned long long)est << 32 | (uint32_t)~l;  // the longest of equal ones
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) key = min(key, __shfl_xor_sync(0xffffffffu, key, off));
+    if (lane == 0) atomicMin(&sh->best, key);
+    __syncthreads();
+    len = (int)~(uint32_t)sh->best;
+    if (blockIdx.x == 0 && tid == 0) p.plan[0] = len;
+  }
+  // Grids of several rounds without split ranges take the longest sequences first.
+  const bool ranked = !p.split && (int)gridDim.x > p.sms && p.B <= kMaxRankedRows;
+  if (ranked) {
+    if (tid < p.B) {
+      int r = 0;
+      for (int b = 0; b < p.B; ++b) r += nt_s[b] > nt_s[tid] || (nt_s[b] == nt_s[tid] && b < tid);
+      order[r] = tid;
+    }
+    __syncthreads();
+  }
+  if (warp == 0) {
+    int base = 0, found = -1, rem = 0;
+    for (int b0 = 0; b0 < p.B && found < 0; b0 += 32) {
+      const int i = b0 + lane;
+      const int b = i < p.B ? (ranked ? order[i] : i) : 0;
+      const int cnt = i < p.B ? ranges_of(nt_s[b], len) * per_range : 0;
+      int incl = cnt;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      const bool hit = (int)blockIdx.x >= base + incl - cnt && (int)blockIdx.x < base + incl;
+      const unsigned m = __ballot_sync(0xffffffffu, hit);
+      if (m) {
+        const int src = __ffs(m) - 1;
+        found = __shfl_sync(0xffffffffu, b, src);
+        rem = (int)blockIdx.x - __shfl_sync(0xffffffffu, base + incl - cnt, src);
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      sh->item_b = found;
+      sh->item_rem = rem;
+    }
+  }
+  fence_async_smem();  // the plan's scratch lies in the ring, which the copies write next
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+  const int b = sh->item_b;
+  if (b < 0) {  // more CTAs than items
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
+  const Geo g = sequence(p, b);
+  const int nr = ranges_of(g.nt, len);
+  const int pair = sh->item_rem % p.npairs, hr = sh->item_rem / p.npairs;
+  const int range = hr % nr, hk = hr / nr;
+  const int per = (g.nt + nr - 1) / nr;
+  const int t0 = range * per;
+  // The 128-byte-swizzled tiles need 1024-byte alignment, which the dynamic
+  // window has on this GPU; were it otherwise, every sequence would fail.
+  const bool aligned_ok = (smem_u32(smem) & 1023u) == 0;
+  const bool alive = aligned_ok && __ldcg(p.status + b) == 0;  // (CTA-uniform below: one thread's view)
+  if (tid == 0) sh->alive = alive;
+  __syncthreads();
+  const int nt = sh->alive ? max(0, min(per, g.nt - t0)) : 0;  // key tiles of this item
+  const int qt0 = 2 * pair;
+  const bool dual = qt0 + 1 < p.nqt;
+  const int zc = g.sl * p.Hkv + hk;
+  const int row0 = g.ks + g.first + t0 * kKeys;  // cache column of the first key
+  const uint64_t lim = p.wait_limit_ns;
+  // ring order: K_0 (and K_1 where the pipes take turns), then V_j, K_{j + la} in turn
+  const int la = dual ? 1 : 2;
+  auto k_idx = [&](int j) { return j < la ? j : 2 * j - la + 1; };
+  auto v_idx = [&](int j) { return j + min(la + j, nt); };
+  auto load = [&](const CUtensorMap* map, int idx, int j) {
+    const int s = idx % kSlots;
+    uint8_t* dst = ring + s * kTile;
+    mbar_arrive_expect_tx(&sh->full[s], kTile);
+    if (D == 128)
+      tma_load_4d(dst, map, &sh->full[s], 0, row0 + j * kKeys, 0, zc);
+    else
+      tma_load_3d(dst, map, &sh->full[s], 0, row0 + j * kKeys, zc);
+  };
+  const bool producer = (warp == 0 || warp == 2) && lane == 0;
+  const bool is_k = warp == 0;
+  int issued = 0;  // tiles this producer has requested
+  if (producer)
+    while (issued < nt && (is_k ? k_idx(issued) : v_idx(issued)) < kSlots) {
+      load(is_k ? &tmk : &tmv, is_k ? k_idx(issued) : v_idx(issued), issued);
+      ++issued;
+    }
+  if (warp >= 4 && nt > 0) {  // query rows -> swizzled shared memory
+    const int tiles = dual ? 2 : 1;
+    for (int i = tid - 128; i < tiles * kQRows * (D / 8); i += 256) {
+      const int c = i % (D / 8), r = i / (D / 8);  // 16-byte chunk, row of both tiles
+      const int gr = qt0 * kQRows + r;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (gr < p.rows)
+        v = __ldg(reinterpret_cast<const uint4*>(
+                      p.q + (((int64_t)b * (p.M + 1) + gr / p.G) * p.Hq + hk * p.G + gr % p.G) * D) +
+                  c);
+      const int rr = r & (kQRows - 1);
+      *reinterpret_cast<uint4*>(q_s + (r / kQRows) * kTile + (c >> 3) * kHalf + rr * 128 +
+                                (((c & 7) ^ (rr & 7)) << 4)) = v;
+    }
+    fence_async_smem();
+  }
+  __syncthreads();
+
+  if (producer) {
+    // ---------------------------------------------------------------- K and V streams
+    bool to = false;
+    for (; issued < nt; ++issued) {
+      const int idx = is_k ? k_idx(issued) : v_idx(issued);
+      if (idx >= kSlots && !mbar_wait(&sh->empty[idx % kSlots], ((idx / kSlots) - 1) & 1, lim)) {
+        to = true;
+        break;
+      }
+      load(is_k ? &tmk : &tmv, idx, issued);
+    }
+    if (to) atomicExch(&sh->timed_out, 1);
+  } else if (warp == 1 && lane == 0 && nt > 0) {
+    // ---------------------------------------------------------------- MMA issue
+    const uint32_t idesc_s = idesc_bf16(128, kKeys, 0), idesc_o = idesc_bf16(128, D, 1);
+    const int n0 = dual ? nt : (nt + 1) / 2, n1 = dual ? nt : nt / 2;  // steps of the pipes
+    auto qk = [&](int q, int i) -> bool {
+      const int idx = k_idx(dual ? i : 2 * i + q), s = idx % kSlots;
+      if (!mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim)) return false;
+      tc_fence_after();
+      const uint64_t da = sw128_desc(smem_u32(q_s + (dual ? q : 0) * kTile), 16);
+      const uint64_t db = sw128_desc(smem_u32(ring + s * kTile), 16);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t off = (uint64_t)((k >> 2) * (kHalf / 16) + (k & 3) * 2);
+        mma_ss(tmem + q * 256, da + off, db + off, idesc_s, k > 0 ? 1u : 0u);
+      }
+      tc_commit(&sh->s_full[q]);
+      if (!dual || q == 1) tc_commit(&sh->empty[s]);
+      return true;
+    };
+    auto pv = [&](int q, int i, int n) -> bool {
+      const int idx = v_idx(dual ? i : 2 * i + q), s = idx % kSlots;
+      if (!mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim)) return false;
+      if (!mbar_wait(&sh->p_full[q], i & 1, lim)) return false;
+      tc_fence_after();
+      const uint64_t db = sw128_desc(smem_u32(ring + s * kTile), kHalf);
+#pragma unroll
+      for (int k = 0; k < kKeys / 16; ++k)
+        mma_ts(tmem + q * 256 + 128, tmem + q * 256 + k * 8, db + (uint64_t)(k * (16 * 128 / 16)), idesc_o,
+               (i > 0 || k > 0) ? 1u : 0u);
+      if (!dual || q == 1) tc_commit(&sh->empty[s]);
+      if (i == n - 1) tc_commit(&sh->o_full[q]);
+      return true;
+    };
+    bool ok = qk(0, 0);
+    if (ok && n1 > 0) ok = qk(1, 0);
+    for (int i = 0; i < n0 && ok; ++i) {
+      ok = pv(0, i, n0);
+      if (ok && i + 1 < n0) ok = qk(0, i + 1);
+      if (ok && i < n1) ok = pv(1, i, n1);
+      if (ok && i + 1 < n1) ok = qk(1, i + 1);
+    }
+    if (!ok) atomicExch(&sh->timed_out, 1);
+    // every MMA issued retires before TMEM and shared memory are released
+    tc_commit(&sh->drain);
+    mbar_wait(&sh->drain, 0);
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax
+    const int pipe = (warp - 4) >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const int qt = dual ? qt0 + pipe : qt0;
+    const int gr = qt * kQRows + r;
+    const bool row_ok = gr < p.rows;
+    const bool warp_live = __any_sync(0xffffffffu, row_ok);
+    const int u = min(gr / p.G, p.M);
+    const int64_t node = (int64_t)b * (p.M + 1) + u;
+    const int32_t* dep_b = p.depth ? p.depth + (int64_t)b * (p.M + 1) : nullptr;
+    const int du = (p.window > 0 || BIAS) && nt > 0 ? __ldg(dep_b + u) : 0;
+    const float slope2 = BIAS ? __ldg(p.slopes + hk * p.G + gr % p.G) * 1.4426950408889634f : 0.f;
+    const int pos = g.kl + du;
+    const int lo = p.window > 0 ? max(0, pos - (p.window - 1)) : 0;  // first prefix key of the row
+    const uint32_t t_s = tmem + pipe * 256 + ((uint32_t)((warp & 3) * 32) << 16), t_o = t_s + 128;
+    const int n = dual ? nt : (pipe == 0 ? (nt + 1) / 2 : nt / 2);
+    float m = TRACK ? -INFINITY : p.ref, l = 0.f;
+    uint64_t l2[2] = {0ull, 0ull};
+    bool to = false;
+    for (int i = 0; i < n; ++i) {
+      const int j = dual ? i : 2 * i + pipe;
+      const int key0 = g.first + (t0 + j) * kKeys;  // of the sequence
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh->s_full[pipe], i & 1, lim))) {
+        to = true;
+        break;
+      }
+      tc_fence_after();
+      if (warp_live) {
+        const bool edge = __any_sync(0xffffffffu, key0 + kKeys > g.kl || key0 < lo);
+        // the keys kc .. kc+31 that the row may read
+        auto allowed = [&](int kc) -> uint32_t {
+          const int np = g.kl - kc;
+          uint32_t w = np >= 32 ? ~0u : (np <= 0 ? 0u : (1u << np) - 1u);
+          if (lo > kc) w &= lo - kc >= 32 ? 0u : ~0u << (lo - kc);
+          const int r0 = kc - g.kl;  // tree row of bit 0
+          if (r0 > -32 && r0 <= p.M) {
+            const uint32_t* a = p.anc + node * p.W;
+            uint32_t t;
+            if (r0 <= 0) {
+              t = __ldg(a) << -r0;
+            } else {
+              const int wi = r0 >> 5, sft = r0 & 31;
+              t = __ldg(a + wi) >> sft;
+              if (sft && wi + 1 < p.W) t |= __ldg(a + wi + 1) << (32 - sft);
+            }
+            if (p.M + 1 - r0 < 32) t &= (1u << (p.M + 1 - r0)) - 1u;
+            if (p.window > 0)
+              for (uint32_t s = t; s; s &= s - 1) {
+                const int bit = __ffs(s) - 1;
+                if (du - __ldg(dep_b + r0 + bit) >= p.window) t &= ~(1u << bit);
+              }
+            w |= t;
+          }
+          return w;
+        };
+        if (TRACK) {
+          // row maximum of the scores; the cap keeps their order
+          float mx = -INFINITY;
+          uint32_t raw[32];
+          float x[32];
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32(t_s + c * 32, raw);
+            const uint32_t ok = edge ? allowed(key0 + 32 * c) : ~0u;
+            tmem_wait_ld32(raw);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(raw[e]);
+            if (BIAS) {
+              chunk_scores<MODE>(x, p, edge, ok, 0.f, slope2, pos, key0 + 32 * c, g.kl, du, dep_b);
+            } else if (edge) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((ok >> e) & 1u)) x[e] = -INFINITY;
+            }
+            float a[2] = {fmaxf(mx, x[0]), x[1]};
+#pragma unroll
+            for (int e = 2; e < 32; e += 2) a[(e >> 1) & 1] = fmax3(a[(e >> 1) & 1], x[e], x[e + 1]);
+            mx = fmaxf(a[0], a[1]);
+          }
+          if (MODE == kPlain) mx *= p.scale_log2;
+          if (MODE == kCapHigh && mx != -INFINITY) mx = cap_score(mx, p);
+          // The reference follows the maximum lazily: O is rescaled (a TMEM access of
+          // the whole warp, each row by its own factor) only when some row's maximum
+          // has grown by more than 2^kGrow.
+          const bool grow = mx > m + kGrow;
+          const bool scale_o = grow && m != -INFINITY;
+          if (__any_sync(0xffffffffu, scale_o)) {
+            const float corr = scale_o ? fast_exp2(m - mx) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(t_o + c * 32, o);
+              tmem_wait_ld32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              tmem_st32(t_o + c * 32, o);
+            }
+            float s0, s1, s2, s3;
+            f2_unpack(l2[0], s0, s1);
+            f2_unpack(l2[1], s2, s3);
+            l = (l + ((s0 + s1) + (s2 + s3))) * corr;
+            l2[0] = l2[1] = 0ull;
+          }
+          if (grow) m = mx;
+        }
+        const float sub = m == -INFINITY ? 0.f : m;
+        uint32_t raw[2][32];
+        tmem_ld32(t_s, raw[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t ok = edge ? allowed(key0 + 32 * c) : ~0u;
+          tmem_wait_ld32(raw[c & 1]);
+          if (c < 3) tmem_ld32(t_s + (c + 1) * 32, raw[(c + 1) & 1]);
+          float x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(raw[c & 1][e]);
+          chunk_scores<MODE>(x, p, edge, ok, sub, slope2, pos, key0 + 32 * c, g.kl, du, dep_b);
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float p0 = fast_exp2(x[2 * e]), p1 = fast_exp2(x[2 * e + 1]);
+            l2[e & 1] = f2_add(l2[e & 1], f2_pack(p0, p1));
+            pk[e] = pack_bf16x2(p0, p1);  // the tensor core takes the weights in bf16
+          }
+          tmem_st16(t_s + c * 16, pk);
+        }
+        tmem_wait_st();
+      }
+      // V rows behind the step's may hold anything: zero them (the first pipe's
+      // warps for both pipes where they share the tile; its PV is issued first)
+      const int kend = g.kl + p.M + 1 - key0;
+      if (kend < kKeys && (!dual || pipe == 0)) {
+        const int idx = v_idx(j), s = idx % kSlots;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim))) {
+          to = true;
+          break;
+        }
+        uint8_t* vt = ring + s * kTile;
+        for (int e = r; e < (kKeys - kend) * (D / 8); e += kQRows) {
+          const int row = kend + e / (D / 8), c = e % (D / 8);
+          *reinterpret_cast<uint4*>(vt + (c >> 3) * kHalf + row * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->p_full[pipe]);
+    }
+    {
+      float s0, s1, s2, s3;
+      f2_unpack(l2[0], s0, s1);
+      f2_unpack(l2[1], s2, s3);
+      l += (s0 + s1) + (s2 + s3);
+    }
+    bool have = n > 0 && !to;
+    if (have && !mbar_wait(&sh->o_full[pipe], 0, lim)) to = true;
+    // (the second pipe's hand-over below goes through the ring: the first one's
+    // tiles must be used as well)
+    if (!dual && nt > 0 && !to && !mbar_wait(&sh->o_full[0], 0, lim)) to = true;
+    have = have && !to;
+    have = __all_sync(0xffffffffu, have);  // gates warp-collective TMEM reads
+    if (to) atomicExch(&sh->timed_out, 1);
+    tc_fence_after();
+    if (!have) {
+      m = -INFINITY;
+      l = 0.f;
+    }
+    // ---------------------------------------------------------------- epilogue
+    // Pipes that shared a query tile join: the second hands its O, reference and
+    // sum to the first through the ring, whose tiles are all used.
+    float4* join_o = reinterpret_cast<float4*>(ring);                      // [D / 4][128]
+    float2* join_ml = reinterpret_cast<float2*>(ring + kQRows * D * 4);    // [128]
+    float w0 = 1.f, w1 = 0.f;
+    if (!dual) {
+      if (pipe == 1) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (have) {
+            tmem_ld32(t_o + c * 32, o);
+            tmem_wait_ld32(o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            join_o[(c * 8 + e) * kQRows + r] =
+                make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                            __uint_as_float(o[4 * e + 3]));
+        }
+        join_ml[r] = make_float2(m, l);
+      }
+      asm volatile("bar.sync 3, 256;" ::: "memory");
+      if (pipe == 0) {
+        const float2 o = join_ml[r];
+        const float mm = fmaxf(m, o.x), ms = mm == -INFINITY ? 0.f : mm;
+        w0 = fast_exp2(m - ms);  // 0 for a pipe without keys
+        w1 = fast_exp2(o.x - ms);
+        l = l * w0 + o.y * w1;
+        m = mm;
+      }
+    }
+    if (dual || pipe == 0) {
+      const bool whole = nr == 1;
+      const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      w0 *= inv;
+      w1 *= inv;
+      uint8_t* stage = q_s + pipe * kTile;  // this pipe's query tile is used: [128 rows][2 D bytes], chunks rotated
+      const int64_t rec = 2 * (int64_t)blockIdx.x + pipe;
+      float4* dst = reinterpret_cast<float4*>(p.ws_o) + rec * (D / 4) * p.rec_rows;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (have) {
+          tmem_ld32(t_o + c * 32, o);
+          tmem_wait_ld32(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        float4 a[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          a[e] = make_float4(__uint_as_float(o[4 * e]) * w0, __uint_as_float(o[4 * e + 1]) * w0,
+                             __uint_as_float(o[4 * e + 2]) * w0, __uint_as_float(o[4 * e + 3]) * w0);
+          if (!dual) {
+            const float4 x = join_o[(c * 8 + e) * kQRows + r];
+            a[e] = make_float4(fmaf(x.x, w1, a[e].x), fmaf(x.y, w1, a[e].y), fmaf(x.z, w1, a[e].z),
+                               fmaf(x.w, w1, a[e].w));
+          }
+        }
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 x = a[2 * e], y = a[2 * e + 1];
+            const int chunk = c * 4 + e;
+            *reinterpret_cast<uint4*>(stage + r * (2 * D) + ((chunk ^ (r & 7)) << 4)) =
+                make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+          }
+        } else if (row_ok) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) __stcg(dst + (int64_t)(c * 8 + e) * p.rec_rows + r, a[e]);
+        }
+      }
+      if (whole) {
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + pipe) : "memory");
+        const int rows = min(kQRows, p.rows - qt * kQRows);
+        const bool fail = *(volatile int*)&sh->timed_out != 0;
+        for (int e = r; e < rows * (D / 8); e += kQRows) {
+          const int rr = e / (D / 8), chunk = e % (D / 8);
+          const int g2 = qt * kQRows + rr;
+          uint4 v = *reinterpret_cast<const uint4*>(stage + rr * (2 * D) + ((chunk ^ (rr & 7)) << 4));
+          if (fail) v = make_uint4(0, 0, 0, 0);
+          reinterpret_cast<uint4*>(p.out + (((int64_t)b * (p.M + 1) + g2 / p.G) * p.Hq + hk * p.G + g2 % p.G) *
+                                               D)[chunk] = v;
+        }
+      } else if (row_ok) {
+        __stcg(p.ws_ml + rec * p.rec_rows + r, make_float2(m, l));
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  // a copy that no MMA waited for must land before the shared memory is released
+  if (producer && sh->timed_out)
+    for (int j = max(0, issued - kSlots); j < issued; ++j) {
+      const int idx = is_k ? k_idx(j) : v_idx(j);
+      mbar_wait(&sh->full[idx % kSlots], (idx / kSlots) & 1);
+    }
+  if (tid == 0) {
+    const int flag = (sh->timed_out || !aligned_ok ? kSeqTimeout : 0) | (g.sl < 0 ? kSeqBadGeometry : 0);
+    if (flag) atomicOr(&p.status[b], flag);
+  }
+}
+
+// Joins the records of sequences whose key range was split: out = sum_i 2^(m_i -
+// m) O_i / sum_i 2^(m_i - m) l_i.  One thread per row and four columns.
+template <int D>
+__global__ void __launch_bounds__(256) scored_merge_kernel(const __grid_constant__ ScoredParams p) {
+  __shared__ int red[8];
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int qt = blockIdx.x % p.nqt, bh = blockIdx.x / p.nqt, hk = bh % p.Hkv, b = bh / p.Hkv;
+  const int len = p.plan[0];
+  const int nr = ranges_of(sequence(p, b).nt, len);
+  if (nr == 1) return;
+  int before = 0;
+  for (int i = threadIdx.x; i < b; i += 256) before += ranges_of(sequence(p, i).nt, len);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = before;
+  __syncthreads();
+  before = 0;
+  for (int i = 0; i < 8; ++i) before += red[i];
+  const int rows = min(kQRows, p.rows - qt * kQRows);
+  const int64_t item0 = ((int64_t)before * p.Hkv + (int64_t)hk * nr) * p.npairs + qt / 2;
+  const int pipe = qt & 1;
+  const bool fail = p.status[b] != 0;
+  const float4* ws_o = reinterpret_cast<const float4*>(p.ws_o);
+  for (int e = blockIdx.y * 256 + threadIdx.x; e < rows * (D / 4); e += gridDim.y * 256) {
+    const int r = e % rows, c = e / rows;
+    float m = -INFINITY, l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int U = 8;  // records in flight
+    for (int i0 = 0; i0 < nr; i0 += U) {
+      float2 ml[U];
+      float4 o[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        ml[i] = make_float2(-INFINITY, 0.f);
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + i < nr) {
+          const int64_t rec = 2 * (item0 + (int64_t)(i0 + i) * p.npairs) + pipe;
+          ml[i] = __ldcg(p.ws_ml + rec * p.rec_rows + r);
+          o[i] = __ldcg(ws_o + (rec * (D / 4) + c) * p.rec_rows + r);
+        }
+      }
+      float mm = m;
+#pragma unroll
+      for (int i = 0; i < U; ++i) mm = fmaxf(mm, ml[i].x);
+      const float ms = mm == -INFINITY ? 0.f : mm;
+      const float w = fast_exp2(m - ms);
+      l *= w;
+      a = make_float4(a.x * w, a.y * w, a.z * w, a.w * w);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const float wi = fast_exp2(ml[i].x - ms);
+        l = fmaf(wi, ml[i].y, l);
+        a = make_float4(fmaf(wi, o[i].x, a.x), fmaf(wi, o[i].y, a.y), fmaf(wi, o[i].z, a.z), fmaf(wi, o[i].w, a.w));
+      }
+      m = mm;
+    }
+    const float inv = !fail && l > 0.f ? 1.f / l : 0.f;
+    const int g2 = qt * kQRows + r;
+    uint2 v = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    if (fail) v = make_uint2(0u, 0u);
+    *reinterpret_cast<uint2*>(p.out + (((int64_t)b * (p.M + 1) + g2 / p.G) * p.Hq + hk * p.G + g2 % p.G) * D + 4 * c) =
+        v;
+  }
+}
+
+// [BH][S_cap][D] bf16 in boxes of 128 rows: 64 columns (D = 64), or both 64-column
+// halves of a row (D = 128), landing as [half][row][128 B], 128-byte swizzle.
+bool encode_scored_map(CUtensorMap* map, const void* base, int64_t BH, int64_t S_cap, int D) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t S = (cuuint64_t)std::max<int64_t>(S_cap, 1);
+  if (D == 128) {
+    cuuint64_t dims[4] = {64, S, 2, (cuuint64_t)BH};
+    cuuint64_t strides[3] = {256, 128, S * 256};
+    cuuint32_t box[4] = {64, (cuuint32_t)kKeys, 2, 1}, estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  cuuint64_t dims[3] = {64, S, (cuuint64_t)BH};
+  cuuint64_t strides[2] = {128, S * 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)kKeys, 1}, estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Grid and workspace of a shape (lengths are known on the device only).
+struct ScoredPlan {
+  int64_t grid;
+  int sms, nqt, npairs, split, cand_step, rec_rows;
+  size_t ml_off, ws_bytes;  // plan word, records, (reference, sum) pairs
+};
+
+tv_status plan_scored(int B, int M, int Hq, int Hkv, int D, int64_t S_cap, int window, ScoredPlan& lp) {
+  int dev = 0;
+  lp.sms = 148;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&lp.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  const int rows = (Hq / Hkv) * (M + 1);
+  lp.nqt = (rows + kQRows - 1) / kQRows;
+  lp.npairs = (lp.nqt + 1) / 2;
+  lp.rec_rows = std::min(kQRows, rows);
+  const int64_t base = (int64_t)B * Hkv * lp.npairs;
+  int64_t keys = std::max<int64_t>(S_cap, 1);
+  if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window - 1 + M + 1);
+  const int64_t tiles = (keys + kKeys - 1) / kKeys;
+  // Ranges are split while the items stay below three rounds of the SMs: shorter
+  // items would balance the SMs further, but their set-up and merge cost more.
+  lp.split = base < 3 * (int64_t)lp.sms && tiles >= 2 * kMinSplitTiles && tiles < (1 << 20);
+  lp.grid = lp.split ? 3 * (int64_t)lp.sms : base;
+  lp.cand_step = (int)((tiles + kThreads - kMinSplitTiles - 2) / (kThreads - kMinSplitTiles - 1));
+  const size_t recs = lp.split ? 2 * (size_t)lp.grid * lp.rec_rows : 0;
+  lp.ml_off = 256 + recs * D * sizeof(float);
+  lp.ws_bytes = lp.split ? lp.ml_off + recs * sizeof(float2) : 0;
+  return TV_OK;
+}
+
+template <int D>
+tv_status launch_scored(int mode, const CUtensorMap& tmk, const CUtensorMap& tmv, const ScoredParams& p,
+                        const ScoredPlan& lp, cudaStream_t s) {
+  auto kern = mode == kPlain     ? scored_kernel<D, kPlain>
+              : mode == kCapLow  ? scored_kernel<D, kCapLow>
+              : mode == kCapHigh ? scored_kernel<D, kCapHigh>
+              : mode == kBias    ? scored_kernel<D, kBias>
+                                 : scored_kernel<D, kCapBias>;
+  const size_t smem = 2 * (D / 64) * kHalf + kRingBytes + sizeof(Shared);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  tv_status r = launch(kern, dim3((unsigned)lp.grid), dim3(kThreads), smem, s, 1, true, tmk, tmv, p);
+  if (r != TV_OK || !lp.split) return r;
+  const int per_tile = (lp.rec_rows * (D / 4) + 255) / 256;
+  return launch(scored_merge_kernel<D>, dim3((unsigned)((int64_t)p.B * p.Hkv * p.nqt), per_tile), dim3(256), 0, s, 1,
+                true, p);
 }
 
 }  // namespace
@@ -85,7 +843,12 @@ __global__ void __launch_bounds__(128) scored_rows_kernel(const __grid_constant_
 
 extern "C" size_t tree_attention_scored_workspace_size(int B, int M, int Hq, int Hkv, int D, int64_t S_cap,
                                                        int window) {
-  return 0;
+  using namespace tv;
+  if (B <= 0 || M < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128) || M + 1 > kMaxRows ||
+      S_cap < 0 || window < 0 || (int64_t)(Hq / Hkv) * (M + 1) > (1 << 24))
+    return 0;
+  ScoredPlan lp;
+  return plan_scored(B, M, Hq, Hkv, D, S_cap, window, lp) == TV_OK ? lp.ws_bytes : 0;
 }
 
 extern "C" tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t S_cap,
@@ -99,15 +862,22 @@ extern "C" tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k,
   if (Hq % Hkv != 0 || window < 0 || !(softcap >= 0.f) || !isfinite(softcap)) return TV_ERR_INVALID_ARG;
   if (slot && n_slots < 1) return TV_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return TV_ERR_UNSUPPORTED;
-  if (M + 1 > kMaxRows || S_cap > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
+  if (M + 1 > kMaxRows || S_cap > 0x7fffffffLL || B > kMaxBatch) return TV_ERR_UNSUPPORTED;
+  // the polynomial's coefficients hold (scale / softcap)^8
+  if (softcap > 0.f && scale / softcap > 1e4f) return TV_ERR_UNSUPPORTED;
+  if ((int64_t)(Hq / Hkv) * (M + 1) > (1 << 24)) return TV_ERR_UNSUPPORTED;
   if (B == 0) return TV_OK;
   if (!q || !k || !v || !kv_start || !kv_len || !anc_mask || !status || !out) return TV_ERR_INVALID_ARG;
   if ((window > 0 || alibi_slopes) && !depth) return TV_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return TV_ERR_INVALID_ARG;
-  ScoredParams p;
+  ScoredPlan lp;
+  tv_status r = plan_scored(B, M, Hq, Hkv, D, S_cap, window, lp);
+  if (r != TV_OK) return r;
+  if (lp.grid > 0x3fffffffLL || (int64_t)B * Hkv * lp.nqt > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
+  if (lp.ws_bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < lp.ws_bytes))
+    return TV_ERR_INVALID_ARG;
+  ScoredParams p = {};
   p.q = q;
-  p.k = k;
-  p.v = v;
   p.kv_start = kv_start;
   p.kv_len = kv_len;
   p.depth = depth;
@@ -117,6 +887,7 @@ extern "C" tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k,
   p.slopes = alibi_slopes;
   p.out = out;
   p.S_cap = S_cap;
+  p.B = B;
   p.M = M;
   p.Hq = Hq;
   p.Hkv = Hkv;
@@ -124,11 +895,38 @@ extern "C" tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k,
   p.W = (M + 1 + 31) / 32;
   p.n_slots = slot ? n_slots : B;
   p.window = window;
-  p.scale = scale;
-  p.cap = softcap;
-  p.rows = (int64_t)B * (M + 1) * Hq;
-  const int64_t blocks = (p.rows + 3) / 4;
-  if (blocks > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
-  auto kern = D == 64 ? scored_rows_kernel<64> : scored_rows_kernel<128>;
-  return launch(kern, dim3((unsigned)blocks), dim3(128), 0, reinterpret_cast<cudaStream_t>(stream), 1, true, p);
+  p.rows = p.G * (M + 1);
+  p.nqt = lp.nqt;
+  p.npairs = lp.npairs;
+  p.rec_rows = lp.rec_rows;
+  p.sms = lp.sms;
+  p.split = lp.split;
+  p.cand_step = lp.cand_step;
+  const double log2e = 1.4426950408889634;
+  p.scale_log2 = (float)(scale * log2e);
+  int mode = alibi_slopes ? kBias : kPlain;
+  if (softcap > 0.f) {
+    const double z = (double)scale / softcap, cap2 = softcap * log2e;
+    double f = scale * log2e;
+    for (int i = 0; i < 5; ++i, f *= z * z) p.c[i] = (float)(kPoly[i] * f);
+    p.x_lim = (float)std::min(kPolyLim / z, 3e38);
+    p.z2 = (float)(2.0 * z * log2e);
+    p.cap_log2 = (float)cap2;
+    mode = alibi_slopes ? kCapBias : (cap2 <= kLowCap ? kCapLow : kCapHigh);
+    // exponents lie in [-cap2 - ref, cap2 - ref], inside [-110, 60]
+    p.ref = (float)std::min(cap2, 110.0 - cap2);
+  }
+  p.wait_limit_ns = pipeline_wait_limit_ns();
+  if (lp.split) {
+    p.plan = static_cast<int*>(workspace);
+    p.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
+    p.ws_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + lp.ml_off);
+  }
+  CUtensorMap tmk, tmv;
+  const int64_t BH = (int64_t)p.n_slots * Hkv;
+  if (BH > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
+  if (!encode_scored_map(&tmk, k, BH, S_cap, D) || !encode_scored_map(&tmv, v, BH, S_cap, D))
+    return record_cuda_error(cudaErrorInvalidValue);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return D == 64 ? launch_scored<64>(mode, tmk, tmv, p, lp, s) : launch_scored<128>(mode, tmk, tmv, p, lp, s);
 }
