@@ -45,6 +45,7 @@ constexpr int kMaxSlots = 10;
 constexpr int kThreads = 384;
 constexpr float kGrow = 8.0f;              // the running maximum follows in steps of more than 2^8
 constexpr int kMaxBatch = 16384;
+constexpr int kMaxRounds = 4;              // items per SM, at most, where ranges are split
 constexpr int kMinSplitTiles = 4;          // key tiles below which a range is not split further
 constexpr int kMaxRankedRows = kThreads;
 
@@ -115,6 +116,7 @@ struct Shared {
   int timed_out;
   int item_b, item_rem;
   int alive;
+  int depth[kMaxRows];
 };
 
 // One capped score (log2) from the raw product x.
@@ -126,20 +128,19 @@ __device__ __forceinline__ float cap_score(float x, const ScoredParams& p) {
   return fabsf(x) <= p.x_lim ? x * g : p.cap_log2 * (1.f - __fdividef(2.f, fast_exp2(x * p.z2) + 1.f));
 }
 
-// 32 scores of a row, minus `sub`, from the raw products x of keys kc .. kc+31.
-// ok: the keys that count (used where `edge`).  slope2, pos: the row's bias per
-// position (log2) and its position.
+// 32 scores of a row, minus `sub`, from the raw products x of keys kc .. kc+31, in
+// the general form.  ok: the keys that count (used where `edge`; what lies behind
+// the step's rows may be anything).  slope2, pos: the row's bias per position
+// (log2) and its position; dep: the tree rows' depths.
 template <int MODE>
 __device__ __forceinline__ void chunk_scores(float (&x)[32], const ScoredParams& p, bool edge, uint32_t ok, float sub,
-                                             float slope2, int pos, int kc, int kl, int du, const int32_t* dep_b) {
+                                             float slope2, int pos, int kc, int kl, int du, const int* dep) {
   constexpr bool CAP = MODE == kCapLow || MODE == kCapHigh || MODE == kCapBias;
   constexpr bool BIAS = MODE == kBias || MODE == kCapBias;
-  if (edge) {  // rows behind the step's may hold anything
+  if (edge) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (!((ok >> j) & 1u)) x[j] = 0.f;
+    for (int j = 0; j < 32; ++j) x[j] = (ok >> j) & 1u ? x[j] : 0.f;
   }
-  const float base = BIAS ? -slope2 * (float)(pos - kc) - sub : -sub;
   bool far = false;
   if (CAP) {
     float a[2] = {fabsf(x[0]), fabsf(x[1])};
@@ -147,39 +148,37 @@ __device__ __forceinline__ void chunk_scores(float (&x)[32], const ScoredParams&
     for (int j = 2; j < 32; j += 2) a[(j >> 1) & 1] = fmax3(a[(j >> 1) & 1], fabsf(x[j]), fabsf(x[j + 1]));
     far = __any_sync(0xffffffffu, fmaxf(a[0], a[1]) > p.x_lim);
   }
-  if (!far && !(BIAS && edge)) {
-    const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), b2 = f2_pack(base, base);
-    const uint64_t sl2 = f2_pack(slope2, slope2);
+  if (far) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x[j] = cap_score(x[j], p);
+  } else {
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const uint64_t v = f2_pack(x[2 * j], x[2 * j + 1]);
-      uint64_t g = sc2;
+      uint64_t g = f2_pack(p.scale_log2, p.scale_log2);
       if (CAP) {
         const uint64_t t = f2_mul(v, v);
         g = f2_pack(p.c[4], p.c[4]);
 #pragma unroll
         for (int i = 3; i >= 0; --i) g = f2_fma(g, t, f2_pack(p.c[i], p.c[i]));
       }
-      const uint64_t add = BIAS ? f2_fma(sl2, f2_pack((float)(2 * j), (float)(2 * j + 1)), b2) : b2;
-      f2_unpack(f2_fma(v, g, add), x[2 * j], x[2 * j + 1]);
+      f2_unpack(f2_mul(v, g), x[2 * j], x[2 * j + 1]);
+    }
+  }
+  if (BIAS && kc + 32 > kl) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const int t = kc + j - kl;  // tree row
+      const int dist = t < 0 ? pos - (kc + j) : du - dep[min(t, p.M)];
+      x[j] += fmaf(-slope2, (float)dist, -sub);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float s = CAP ? cap_score(x[j], p) : x[j] * p.scale_log2;
-      float add = -sub;
-      if (BIAS) {
-        int dist = pos - (kc + j);
-        if (edge && kc + j >= kl) dist = du - (kc + j - kl <= p.M ? __ldg(dep_b + (kc + j - kl)) : 0);
-        add = fmaf(-slope2, (float)dist, -sub);
-      }
-      x[j] = s + add;
-    }
+    for (int j = 0; j < 32; ++j) x[j] += BIAS ? fmaf(-slope2, (float)(pos - (kc + j)), -sub) : -sub;
   }
   if (edge) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (!((ok >> j) & 1u)) x[j] = -INFINITY;
+    for (int j = 0; j < 32; ++j) x[j] = (ok >> j) & 1u ? x[j] : -INFINITY;
   }
 }
 
@@ -188,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     scored_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const __grid_constant__ ScoredParams p) {
   constexpr bool BIAS = MODE == kBias || MODE == kCapBias;
+  constexpr bool CAP = MODE == kCapLow || MODE == kCapHigh || MODE == kCapBias;
   constexpr bool TRACK = MODE != kCapLow;  // a running maximum is kept
   constexpr int kHalves = D / 64;
   constexpr int kTile = kHalves * kHalf;  // K, V or Q tile
@@ -226,10 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---------------------------------------------------------------- which item
   // Every CTA forms the same plan from the sequences' lengths: the number of key
-  // tiles per range that finishes first by this estimate (in steps of a pipe
-  // pair): rounds of items on the SMs x steps of an item, 3 steps of set-up and
-  // epilogue a round, 3 for the merge where ranges are split.  Each thread tries
-  // one length.
+  // tiles per range that finishes first by this estimate, in steps of a pipe
+  // pair: the steps of an item, or of an SM's share of all of them, 3 steps of
+  // set-up and epilogue a round of items, 3 for the merge where ranges are
+  // split.  Each thread tries one length.
   int* nt_s = reinterpret_cast<int*>(ring);
   int* order = nt_s + p.B;
   for (int b = tid; b < p.B; b += kThreads) nt_s[b] = sequence(p, b).nt;
@@ -247,9 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned long long key = ~0ull;
     if (items <= (int64_t)gridDim.x) {
       const int64_t half_items = ranges * p.Hkv * p.nqt;  // a lone query tile takes half the steps
-      const int64_t rounds = p.nqt > 1 ? (half_items + 2 * p.sms - 1) / (2 * p.sms) : (items + p.sms - 1) / p.sms;
       const int64_t steps = p.nqt > 1 ? l : (l + 1) / 2;
-      const int64_t est = rounds * steps + 3 * ((items + p.sms - 1) / p.sms) + (ranges > p.B ? 3 : 0);
+      // items that do not start at once leave the SMs uneven by half an item
+      const int64_t run = items <= p.sms ? steps : half_items * l / (2 * p.sms) + steps / 2;
+      const int64_t est = run + 3 * ((items + p.sms - 1) / p.sms) + (ranges > p.B ? 3 : 0);
       key = (unsigned long long)est << 32 | (uint32_t)~l;  // the longest of equal ones
     }
 #pragma unroll
@@ -323,6 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int zc = g.sl * p.Hkv + hk;
   const int row0 = g.ks + g.first + t0 * kKeys;  // cache column of the first key
   const uint64_t lim = p.wait_limit_ns;
+  // Key tiles are taken from the last to the first: with a bias by distance the
+  // largest scores come first, and the reference seldom moves.
   // ring order: K_0 (and K_1 where the pipes take turns), then V_j, K_{j + la} in turn
   const int la = dual ? 1 : 2;
   auto k_idx = [&](int j) { return j < la ? j : 2 * j - la + 1; };
@@ -332,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* dst = ring + s * kTile;
     mbar_arrive_expect_tx(&sh->full[s], kTile);
     if (D == 128)
-      tma_load_4d(dst, map, &sh->full[s], 0, row0 + j * kKeys, 0, zc);
+      tma_load_4d(dst, map, &sh->full[s], 0, row0 + (nt - 1 - j) * kKeys, 0, zc);
     else
-      tma_load_3d(dst, map, &sh->full[s], 0, row0 + j * kKeys, zc);
+      tma_load_3d(dst, map, &sh->full[s], 0, row0 + (nt - 1 - j) * kKeys, zc);
   };
   const bool producer = (warp == 0 || warp == 2) && lane == 0;
   const bool is_k = warp == 0;
@@ -358,6 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       *reinterpret_cast<uint4*>(q_s + (r / kQRows) * kTile + (c >> 3) * kHalf + rr * 128 +
                                 (((c & 7) ^ (rr & 7)) << 4)) = v;
     }
+    if (p.depth)
+      for (int i = tid - 128; i <= p.M; i += 256) sh->depth[i] = __ldg(p.depth + (int64_t)b * (p.M + 1) + i);
     fence_async_smem();
   }
   __syncthreads();
@@ -429,8 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool warp_live = __any_sync(0xffffffffu, row_ok);
     const int u = min(gr / p.G, p.M);
     const int64_t node = (int64_t)b * (p.M + 1) + u;
-    const int32_t* dep_b = p.depth ? p.depth + (int64_t)b * (p.M + 1) : nullptr;
-    const int du = (p.window > 0 || BIAS) && nt > 0 ? __ldg(dep_b + u) : 0;
+    const int du = (p.window > 0 || BIAS) && nt > 0 ? sh->depth[u] : 0;
     const float slope2 = BIAS ? __ldg(p.slopes + hk * p.G + gr % p.G) * 1.4426950408889634f : 0.f;
     const int pos = g.kl + du;
     const int lo = p.window > 0 ? max(0, pos - (p.window - 1)) : 0;  // first prefix key of the row
@@ -441,116 +445,160 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool to = false;
     for (int i = 0; i < n; ++i) {
       const int j = dual ? i : 2 * i + pipe;
-      const int key0 = g.first + (t0 + j) * kKeys;  // of the sequence
       if (!__all_sync(0xffffffffu, mbar_wait(&sh->s_full[pipe], i & 1, lim))) {
         to = true;
         break;
       }
       tc_fence_after();
       if (warp_live) {
+        const int key0 = g.first + (t0 + nt - 1 - j) * kKeys;  // of the sequence
         const bool edge = __any_sync(0xffffffffu, key0 + kKeys > g.kl || key0 < lo);
-        // the keys kc .. kc+31 that the row may read
-        auto allowed = [&](int kc) -> uint32_t {
-          const int np = g.kl - kc;
-          uint32_t w = np >= 32 ? ~0u : (np <= 0 ? 0u : (1u << np) - 1u);
-          if (lo > kc) w &= lo - kc >= 32 ? 0u : ~0u << (lo - kc);
-          const int r0 = kc - g.kl;  // tree row of bit 0
-          if (r0 > -32 && r0 <= p.M) {
-            const uint32_t* a = p.anc + node * p.W;
-            uint32_t t;
-            if (r0 <= 0) {
-              t = __ldg(a) << -r0;
-            } else {
-              const int wi = r0 >> 5, sft = r0 & 31;
-              t = __ldg(a + wi) >> sft;
-              if (sft && wi + 1 < p.W) t |= __ldg(a + wi + 1) << (32 - sft);
-            }
-            if (p.M + 1 - r0 < 32) t &= (1u << (p.M + 1 - r0)) - 1u;
-            if (p.window > 0)
-              for (uint32_t s = t; s; s &= s - 1) {
-                const int bit = __ffs(s) - 1;
-                if (du - __ldg(dep_b + r0 + bit) >= p.window) t &= ~(1u << bit);
+        bool done = false;
+        // A tile inside the prefix, in one pass over S with the reference at hand;
+        // the weights stay in registers until the warp knows that every score lay in
+        // the polynomial's range and below the reference's headroom.  S is still there
+        // for the general path if not.
+        if (!edge && (!TRACK || i > 0)) {
+          const float sub = m == -INFINITY ? 0.f : m;
+          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+          const uint64_t step2 = f2_pack(2.f * slope2, 2.f * slope2);
+          uint64_t ls[2] = {l2[0], l2[1]};
+          float am[2] = {0.f, 0.f}, sm[2] = {-INFINITY, -INFINITY};
+          uint32_t raw[2][32], pk[2][32];
+          tmem_ld32(t_s, raw[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t(&x)[32] = raw[c & 1];
+            tmem_wait_ld32(x);
+            if (c < 3) tmem_ld32(t_s + (c + 1) * 32, raw[(c + 1) & 1]);
+            const float base = BIAS ? -slope2 * (float)(pos - key0 - 32 * c) - sub : -sub;
+            uint64_t add = f2_pack(base, base);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x0 = __uint_as_float(x[2 * e]), x1 = __uint_as_float(x[2 * e + 1]);
+              const uint64_t v = f2_pack(x0, x1);
+              uint64_t gf = sc2;
+              if (CAP) {
+                const uint64_t t = f2_mul(v, v);
+                gf = f2_pack(p.c[4], p.c[4]);
+#pragma unroll
+                for (int d = 3; d >= 0; --d) gf = f2_fma(gf, t, f2_pack(p.c[d], p.c[d]));
+                am[e & 1] = fmax3(am[e & 1], fabsf(x0), fabsf(x1));
               }
-            w |= t;
+              if (BIAS)
+                add = (e & 3) == 0 ? f2_pack(fmaf(slope2, (float)(2 * e), base), fmaf(slope2, (float)(2 * e + 1), base))
+                                   : f2_add(add, step2);
+              float a0, a1;
+              f2_unpack(f2_fma(v, gf, add), a0, a1);
+              if (TRACK) sm[e & 1] = fmax3(sm[e & 1], a0, a1);
+              const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+              ls[e & 1] = f2_add(ls[e & 1], f2_pack(p0, p1));
+              pk[c >> 1][(c & 1) * 16 + e] = pack_bf16x2(p0, p1);  // the tensor core takes the weights in bf16
+            }
           }
-          return w;
-        };
-        if (TRACK) {
-          // row maximum of the scores; the cap keeps their order
-          float mx = -INFINITY;
-          uint32_t raw[32];
-          float x[32];
+          const bool redo = (CAP && fmaxf(am[0], am[1]) > p.x_lim) || (TRACK && fmaxf(sm[0], sm[1]) > kGrow);
+          if (!__any_sync(0xffffffffu, redo)) {
+            tmem_st32(t_s, pk[0]);
+            tmem_st32(t_s + 32, pk[1]);
+            l2[0] = ls[0];
+            l2[1] = ls[1];
+            done = true;
+          }
+        }
+        if (!done) {
+          // the keys kc .. kc+31 that the row may read
+          auto allowed = [&](int kc) -> uint32_t {
+            const int np = g.kl - kc;
+            uint32_t w = np >= 32 ? ~0u : (np <= 0 ? 0u : (1u << np) - 1u);
+            if (lo > kc) w &= lo - kc >= 32 ? 0u : ~0u << (lo - kc);
+            const int r0 = kc - g.kl;  // tree row of bit 0
+            if (r0 > -32 && r0 <= p.M) {
+              const uint32_t* a = p.anc + node * p.W;
+              uint32_t t;
+              if (r0 <= 0) {
+                t = __ldg(a) << -r0;
+              } else {
+                const int wi = r0 >> 5, sft = r0 & 31;
+                t = __ldg(a + wi) >> sft;
+                if (sft && wi + 1 < p.W) t |= __ldg(a + wi + 1) << (32 - sft);
+              }
+              if (p.M + 1 - r0 < 32) t &= (1u << (p.M + 1 - r0)) - 1u;
+              if (p.window > 0)
+                for (uint32_t s = t; s; s &= s - 1) {
+                  const int bit = __ffs(s) - 1;
+                  if (du - sh->depth[r0 + bit] >= p.window) t &= ~(1u << bit);
+                }
+              w |= t;
+            }
+            return w;
+          };
+          if (TRACK) {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t raw[32];
+              tmem_ld32(t_s + c * 32, raw);
+              const uint32_t ok = edge ? allowed(key0 + 32 * c) : ~0u;
+              tmem_wait_ld32(raw);
+              float x[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(raw[e]);
+              chunk_scores<MODE>(x, p, edge, ok, 0.f, slope2, pos, key0 + 32 * c, g.kl, du, sh->depth);
+              float a[2] = {fmaxf(mx, x[0]), x[1]};
+#pragma unroll
+              for (int e = 2; e < 32; e += 2) a[(e >> 1) & 1] = fmax3(a[(e >> 1) & 1], x[e], x[e + 1]);
+              mx = fmaxf(a[0], a[1]);
+            }
+            // The reference follows the maximum lazily: O is rescaled (a TMEM access of
+            // the whole warp, each row by its own factor) only when some row's maximum
+            // has grown by more than 2^kGrow.  A full S says that O is not in use.
+            const bool grow = mx > m + kGrow;
+            const bool scale_o = grow && m != -INFINITY;
+            if (__any_sync(0xffffffffu, scale_o)) {
+              const float corr = scale_o ? fast_exp2(m - mx) : 1.f;
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(t_o + c * 32, o);
+                tmem_wait_ld32(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                tmem_st32(t_o + c * 32, o);
+              }
+              float s0, s1, s2, s3;
+              f2_unpack(l2[0], s0, s1);
+              f2_unpack(l2[1], s2, s3);
+              l = (l + ((s0 + s1) + (s2 + s3))) * corr;
+              l2[0] = l2[1] = 0ull;
+            }
+            if (grow) m = mx;
+          }
+          const float sub = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
+            uint32_t raw[32];
             tmem_ld32(t_s + c * 32, raw);
             const uint32_t ok = edge ? allowed(key0 + 32 * c) : ~0u;
             tmem_wait_ld32(raw);
+            float x[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(raw[e]);
-            if (BIAS) {
-              chunk_scores<MODE>(x, p, edge, ok, 0.f, slope2, pos, key0 + 32 * c, g.kl, du, dep_b);
-            } else if (edge) {
+            chunk_scores<MODE>(x, p, edge, ok, sub, slope2, pos, key0 + 32 * c, g.kl, du, sh->depth);
+            uint32_t pk[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((ok >> e) & 1u)) x[e] = -INFINITY;
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = fast_exp2(x[2 * e]), p1 = fast_exp2(x[2 * e + 1]);
+              l2[e & 1] = f2_add(l2[e & 1], f2_pack(p0, p1));
+              pk[e] = pack_bf16x2(p0, p1);
             }
-            float a[2] = {fmaxf(mx, x[0]), x[1]};
-#pragma unroll
-            for (int e = 2; e < 32; e += 2) a[(e >> 1) & 1] = fmax3(a[(e >> 1) & 1], x[e], x[e + 1]);
-            mx = fmaxf(a[0], a[1]);
+            tmem_st16(t_s + c * 16, pk);
           }
-          if (MODE == kPlain) mx *= p.scale_log2;
-          if (MODE == kCapHigh && mx != -INFINITY) mx = cap_score(mx, p);
-          // The reference follows the maximum lazily: O is rescaled (a TMEM access of
-          // the whole warp, each row by its own factor) only when some row's maximum
-          // has grown by more than 2^kGrow.
-          const bool grow = mx > m + kGrow;
-          const bool scale_o = grow && m != -INFINITY;
-          if (__any_sync(0xffffffffu, scale_o)) {
-            const float corr = scale_o ? fast_exp2(m - mx) : 1.f;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(t_o + c * 32, o);
-              tmem_wait_ld32(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-              tmem_st32(t_o + c * 32, o);
-            }
-            float s0, s1, s2, s3;
-            f2_unpack(l2[0], s0, s1);
-            f2_unpack(l2[1], s2, s3);
-            l = (l + ((s0 + s1) + (s2 + s3))) * corr;
-            l2[0] = l2[1] = 0ull;
-          }
-          if (grow) m = mx;
-        }
-        const float sub = m == -INFINITY ? 0.f : m;
-        uint32_t raw[2][32];
-        tmem_ld32(t_s, raw[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t ok = edge ? allowed(key0 + 32 * c) : ~0u;
-          tmem_wait_ld32(raw[c & 1]);
-          if (c < 3) tmem_ld32(t_s + (c + 1) * 32, raw[(c + 1) & 1]);
-          float x[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(raw[c & 1][e]);
-          chunk_scores<MODE>(x, p, edge, ok, sub, slope2, pos, key0 + 32 * c, g.kl, du, dep_b);
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float p0 = fast_exp2(x[2 * e]), p1 = fast_exp2(x[2 * e + 1]);
-            l2[e & 1] = f2_add(l2[e & 1], f2_pack(p0, p1));
-            pk[e] = pack_bf16x2(p0, p1);  // the tensor core takes the weights in bf16
-          }
-          tmem_st16(t_s + c * 16, pk);
         }
         tmem_wait_st();
       }
       // V rows behind the step's may hold anything: zero them (the first pipe's
       // warps for both pipes where they share the tile; its PV is issued first)
-      const int kend = g.kl + p.M + 1 - key0;
+      const int kend = g.kl + p.M + 1 - (g.first + (t0 + nt - 1 - j) * kKeys);
       if (kend < kKeys && (!dual || pipe == 0)) {
         const int idx = v_idx(j), s = idx % kSlots;
         if (!__all_sync(0xffffffffu, mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim))) {
@@ -809,10 +857,10 @@ tv_status plan_scored(int B, int M, int Hq, int Hkv, int D, int64_t S_cap, int w
   int64_t keys = std::max<int64_t>(S_cap, 1);
   if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window - 1 + M + 1);
   const int64_t tiles = (keys + kKeys - 1) / kKeys;
-  // Ranges are split while the items stay below three rounds of the SMs: shorter
+  // Ranges are split while the items stay below kMaxRounds rounds of the SMs: shorter
   // items would balance the SMs further, but their set-up and merge cost more.
-  lp.split = base < 3 * (int64_t)lp.sms && tiles >= 2 * kMinSplitTiles && tiles < (1 << 20);
-  lp.grid = lp.split ? 3 * (int64_t)lp.sms : base;
+  lp.split = base < kMaxRounds * (int64_t)lp.sms && tiles >= 2 * kMinSplitTiles && tiles < (1 << 20);
+  lp.grid = lp.split ? kMaxRounds * (int64_t)lp.sms : base;
   lp.cand_step = (int)((tiles + kThreads - kMinSplitTiles - 2) / (kThreads - kMinSplitTiles - 1));
   const size_t recs = lp.split ? 2 * (size_t)lp.grid * lp.rec_rows : 0;
   lp.ml_off = 256 + recs * D * sizeof(float);
