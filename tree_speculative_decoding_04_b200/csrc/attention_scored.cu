@@ -43,9 +43,12 @@ constexpr int kHalf = kKeys * 128;         // one 64-column half of a tile: 128 
 constexpr int kRingBytes = 163840;
 constexpr int kMaxSlots = 10;
 constexpr int kThreads = 384;
-constexpr float kGrow = 8.0f;              // the running maximum follows in steps of more than 2^8
+// A row's reference moves once a score lies more than 2^kGrow above it (the
+// weights are floats in bf16 and sums in fp32: a large weight is as exact as a
+// small one, and 2^24 leaves both far from their limits).
+constexpr float kGrow = 24.0f;
 constexpr int kMaxBatch = 16384;
-constexpr int kMaxRounds = 4;              // items per SM, at most, where ranges are split
+constexpr int kMaxRounds = 6;              // items per SM, at most, where ranges are split
 constexpr int kMinSplitTiles = 4;          // key tiles below which a range is not split further
 constexpr int kMaxRankedRows = kThreads;
 
@@ -74,9 +77,10 @@ struct ScoredParams {
   int rows;         // G * (M + 1) query rows of a (sequence, kv head)
   int nqt, npairs;  // query tiles, and items' pairs of them
   int rec_rows;     // rows of a partial record
-  int sms;
+  int64_t max_items;
   int split;        // key ranges may be split over items
   int cand_step;    // range lengths tried: kMinSplitTiles + i * cand_step tiles
+  float inv_g;      // 1 / G
   float scale_log2, ref;
   float c[5];       // capped score = x * (c0 + c1 x^2 + ...), x = q.k
   float x_lim, z2, cap_log2;  // |x| of the polynomial's range; e^2z = 2^(z2 x); cap * log2e
@@ -107,17 +111,38 @@ __device__ __forceinline__ Geo sequence(const ScoredParams& p, int b) {
 
 __device__ __forceinline__ int ranges_of(int nt, int len) { return nt <= len ? 1 : (nt + len - 1) / len; }
 
+// One item: a pair of query tiles (or a last one alone) and a range of key tiles.
+struct Item {
+  int index;  // -1: no more
+  int b, hk, qt0, dual, nr;  // nr: ranges of the sequence
+  int kl, first, sl;         // first: the range's first key
+  int nt;                    // key tiles (0: nothing to compute, zero rows)
+  int row0;                  // cache column of the first key
+};
+
 struct Shared {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2], o_full[2], q_full;
+  uint64_t item_full[2], item_empty[2];
   uint64_t drain;
   unsigned long long best;
   uint32_t tmem;
-  int timed_out;
-  int item_b, item_rem;
-  int alive;
-  int depth[kMaxRows];
+  int failed;
+  Item item[2];
+  float2 join_ml[kQRows];
+  uint16_t order[kMaxRankedRows];
+  uint8_t depth[kMaxRows];
 };
+constexpr int kItemReaders = 3 + 8;  // both producers, the MMA thread, the softmax warps
+static_assert(4 * kHalf + kRingBytes + sizeof(Shared) <= 232448, "shared memory of a CTA");
+
+// Row of q and out ([B][M+1][Hq]) of the gr-th query row of (b, hk).  gr / G by a
+// reciprocal: exact for G (M+1) < 2^21, which the host checks.
+__device__ __forceinline__ int node_of(const ScoredParams& p, int gr) { return (int)(((float)gr + 0.5f) * p.inv_g); }
+__device__ __forceinline__ int64_t query_row(const ScoredParams& p, int b, int hk, int gr) {
+  const int node = node_of(p, gr);
+  return ((int64_t)b * (p.M + 1) + node) * p.Hq + hk * p.G + (gr - node * p.G);
+}
 
 // One capped score (log2) from the raw product x.
 __device__ __forceinline__ float cap_score(float x, const ScoredParams& p) {
@@ -134,7 +159,7 @@ __device__ __forceinline__ float cap_score(float x, const ScoredParams& p) {
 // (log2) and its position; dep: the tree rows' depths.
 template <int MODE>
 __device__ __forceinline__ void chunk_scores(float (&x)[32], const ScoredParams& p, bool edge, uint32_t ok, float sub,
-                                             float slope2, int pos, int kc, int kl, int du, const int* dep) {
+                                             float slope2, int pos, int kc, int kl, int du, const uint8_t* dep) {
   constexpr bool CAP = MODE == kCapLow || MODE == kCapHigh || MODE == kCapBias;
   constexpr bool BIAS = MODE == kBias || MODE == kCapBias;
   if (edge) {
@@ -169,7 +194,7 @@ __device__ __forceinline__ void chunk_scores(float (&x)[32], const ScoredParams&
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       const int t = kc + j - kl;  // tree row
-      const int dist = t < 0 ? pos - (kc + j) : du - dep[min(t, p.M)];
+      const int dist = t < 0 ? pos - (kc + j) : du - (int)dep[min(t, p.M)];
       x[j] += fmaf(-slope2, (float)dist, -sub);
     }
   } else {
@@ -200,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    sh->timed_out = 0;
+    sh->failed = 0;
     sh->best = ~0ull;
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&sh->full[s], 1);
@@ -211,6 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->p_full[q], 4);
       mbar_init(&sh->o_full[q], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->item_full[i], 1);
+      mbar_init(&sh->item_empty[i], kItemReaders);
+    }
+    mbar_init(&sh->q_full, 8);
     mbar_init(&sh->drain, 1);
     fence_mbar_init();
     prefetch_tensormap(&tmk);
@@ -224,33 +254,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait_primary();
   pdl_launch_dependents();
 
-  // ---------------------------------------------------------------- which item
+  // ---------------------------------------------------------------- the plan
   // Every CTA forms the same plan from the sequences' lengths: the number of key
   // tiles per range that finishes first by this estimate, in steps of a pipe
-  // pair: the steps of an item, or of an SM's share of all of them, 3 steps of
-  // set-up and epilogue a round of items, 3 for the merge where ranges are
-  // split.  Each thread tries one length.
+  // pair: the items of a CTA one after another, 2 steps of set-up and epilogue
+  // each, 3 for the merge where ranges are split.  Each thread tries one length.
   int* nt_s = reinterpret_cast<int*>(ring);
-  int* order = nt_s + p.B;
   for (int b = tid; b < p.B; b += kThreads) nt_s[b] = sequence(p, b).nt;
   __syncthreads();
   int len = INT_MAX;
   const int per_range = p.Hkv * p.npairs;  // items of one key range of a sequence
   if (p.split) {
     const int l = kMinSplitTiles + tid * p.cand_step;
-    // ceil(nt / l) by a reciprocal: exact while nt * 2^2 < 2^23, which the host's
-    // limit on split ranges ensures
+    // ceil(nt / l) by a reciprocal: exact for nt < 2^21, which the host's limit on
+    // split ranges ensures
     const float inv = 1.f / (float)l, up = (float)l - 0.5f;
     int64_t ranges = 0;
     for (int b = 0; b < p.B; ++b) ranges += max(1, (int)(((float)nt_s[b] + up) * inv));
     const int64_t items = ranges * per_range;
     unsigned long long key = ~0ull;
-    if (items <= (int64_t)gridDim.x) {
-      const int64_t half_items = ranges * p.Hkv * p.nqt;  // a lone query tile takes half the steps
+    if (items <= p.max_items) {
       const int64_t steps = p.nqt > 1 ? l : (l + 1) / 2;
-      // items that do not start at once leave the SMs uneven by half an item
-      const int64_t run = items <= p.sms ? steps : half_items * l / (2 * p.sms) + steps / 2;
-      const int64_t est = run + 3 * ((items + p.sms - 1) / p.sms) + (ranges > p.B ? 3 : 0);
+      const int64_t rounds = (items + gridDim.x - 1) / gridDim.x;
+      // a lone query tile takes half the steps of a pair
+      const int64_t mean = (ranges * p.Hkv * p.nqt * l) / (2 * gridDim.x);
+      const int64_t est = min(rounds * steps, mean + steps) + 2 * rounds + (ranges > p.B ? 3 : 0);
       key = (unsigned long long)est << 32 | (uint32_t)~l;  // the longest of equal ones
     }
 #pragma unroll
@@ -260,198 +288,261 @@ __global__ void __launch_bounds__(kThreads, 1)
     len = (int)~(uint32_t)sh->best;
     if (blockIdx.x == 0 && tid == 0) p.plan[0] = len;
   }
-  // Grids of several rounds without split ranges take the longest sequences first.
-  const bool ranked = !p.split && (int)gridDim.x > p.sms && p.B <= kMaxRankedRows;
+  // Whole sequences in several rounds: the longest first.
+  const bool ranked = !p.split && p.max_items > (int64_t)gridDim.x && p.B <= kMaxRankedRows;
   if (ranked) {
     if (tid < p.B) {
       int r = 0;
       for (int b = 0; b < p.B; ++b) r += nt_s[b] > nt_s[tid] || (nt_s[b] == nt_s[tid] && b < tid);
-      order[r] = tid;
+      sh->order[r] = (uint16_t)tid;
     }
     __syncthreads();
   }
-  if (warp == 0) {
-    int base = 0, found = -1, rem = 0;
-    for (int b0 = 0; b0 < p.B && found < 0; b0 += 32) {
+  // Item `index`, by warp 3; the first one reads the plan's scratch.
+  const bool aligned_ok = (smem_u32(smem) & 1023u) == 0;  // the swizzled tiles need it (else all sequences fail)
+  auto decode = [&](int index, bool scratch) -> Item {
+    Item it = {};
+    it.index = -1;
+    int base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int i = b0 + lane;
-      const int b = i < p.B ? (ranked ? order[i] : i) : 0;
-      const int cnt = i < p.B ? ranges_of(nt_s[b], len) * per_range : 0;
+      const int b = i < p.B ? (ranked ? sh->order[i] : i) : 0;
+      const int cnt = i < p.B ? ranges_of(scratch ? nt_s[b] : sequence(p, b).nt, len) * per_range : 0;
       int incl = cnt;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += o;
       }
-      const bool hit = (int)blockIdx.x >= base + incl - cnt && (int)blockIdx.x < base + incl;
-      const unsigned m = __ballot_sync(0xffffffffu, hit);
+      const unsigned m = __ballot_sync(0xffffffffu, index < base + incl);
       if (m) {
         const int src = __ffs(m) - 1;
-        found = __shfl_sync(0xffffffffu, b, src);
-        rem = (int)blockIdx.x - __shfl_sync(0xffffffffu, base + incl - cnt, src);
+        it.b = __shfl_sync(0xffffffffu, b, src);
+        const int rem = index - __shfl_sync(0xffffffffu, base + incl - cnt, src);
+        const Geo g = sequence(p, it.b);
+        it.index = index;
+        it.nr = ranges_of(g.nt, len);
+        it.qt0 = 2 * (rem % p.npairs);
+        it.dual = it.qt0 + 1 < p.nqt;
+        const int range = rem / p.npairs % it.nr;
+        it.hk = rem / p.npairs / it.nr;
+        const int per = (g.nt + it.nr - 1) / it.nr;
+        it.sl = g.sl;
+        it.kl = g.kl;
+        it.first = g.first + range * per * kKeys;
+        it.row0 = g.ks + it.first;
+        it.nt = aligned_ok && __ldcg(p.status + it.b) == 0 ? max(0, min(per, g.nt - range * per)) : 0;
+        return it;
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) {
-      sh->item_b = found;
-      sh->item_rem = rem;
-    }
+    return it;
+  };
+  if (warp == 3) {
+    const Item it = decode(blockIdx.x, true);
+    if (lane == 0) sh->item[0] = it;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->item_full[0]);
   }
   fence_async_smem();  // the plan's scratch lies in the ring, which the copies write next
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh->tmem;
-  const int b = sh->item_b;
-  if (b < 0) {  // more CTAs than items
-    if (warp == 1) tmem_dealloc(tmem, 512);
-    return;
-  }
-  const Geo g = sequence(p, b);
-  const int nr = ranges_of(g.nt, len);
-  const int pair = sh->item_rem % p.npairs, hr = sh->item_rem / p.npairs;
-  const int range = hr % nr, hk = hr / nr;
-  const int per = (g.nt + nr - 1) / nr;
-  const int t0 = range * per;
-  // The 128-byte-swizzled tiles need 1024-byte alignment, which the dynamic
-  // window has on this GPU; were it otherwise, every sequence would fail.
-  const bool aligned_ok = (smem_u32(smem) & 1023u) == 0;
-  const bool alive = aligned_ok && __ldcg(p.status + b) == 0;  // (CTA-uniform below: one thread's view)
-  if (tid == 0) sh->alive = alive;
-  __syncthreads();
-  const int nt = sh->alive ? max(0, min(per, g.nt - t0)) : 0;  // key tiles of this item
-  const int qt0 = 2 * pair;
-  const bool dual = qt0 + 1 < p.nqt;
-  const int zc = g.sl * p.Hkv + hk;
-  const int row0 = g.ks + g.first + t0 * kKeys;  // cache column of the first key
   const uint64_t lim = p.wait_limit_ns;
-  // Key tiles are taken from the last to the first: with a bias by distance the
-  // largest scores come first, and the reference seldom moves.
-  // ring order: K_0 (and K_1 where the pipes take turns), then V_j, K_{j + la} in turn
-  const int la = dual ? 1 : 2;
-  auto k_idx = [&](int j) { return j < la ? j : 2 * j - la + 1; };
-  auto v_idx = [&](int j) { return j + min(la + j, nt); };
-  auto load = [&](const CUtensorMap* map, int idx, int j) {
-    const int s = idx % kSlots;
-    uint8_t* dst = ring + s * kTile;
-    mbar_arrive_expect_tx(&sh->full[s], kTile);
-    if (D == 128)
-      tma_load_4d(dst, map, &sh->full[s], 0, row0 + (nt - 1 - j) * kKeys, 0, zc);
-    else
-      tma_load_3d(dst, map, &sh->full[s], 0, row0 + (nt - 1 - j) * kKeys, zc);
+  // Waits for a role's `n`-th item.  An item list is short of nothing the GPU has to
+  // wait for, so this wait keeps the full limit; if it runs out, the role stops.
+  auto next_item = [&](int n) -> Item {
+    Item it = {};
+    it.index = -1;
+    if (mbar_wait(&sh->item_full[n & 1], (n >> 1) & 1)) it = sh->item[n & 1];
+    return it;
   };
-  const bool producer = (warp == 0 || warp == 2) && lane == 0;
-  const bool is_k = warp == 0;
-  int issued = 0;  // tiles this producer has requested
-  if (producer)
-    while (issued < nt && (is_k ? k_idx(issued) : v_idx(issued)) < kSlots) {
-      load(is_k ? &tmk : &tmv, is_k ? k_idx(issued) : v_idx(issued), issued);
-      ++issued;
-    }
-  if (warp >= 4 && nt > 0) {  // query rows -> swizzled shared memory
-    const int tiles = dual ? 2 : 1;
-    for (int i = tid - 128; i < tiles * kQRows * (D / 8); i += 256) {
-      const int c = i % (D / 8), r = i / (D / 8);  // 16-byte chunk, row of both tiles
-      const int gr = qt0 * kQRows + r;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (gr < p.rows)
-        v = __ldg(reinterpret_cast<const uint4*>(
-                      p.q + (((int64_t)b * (p.M + 1) + gr / p.G) * p.Hq + hk * p.G + gr % p.G) * D) +
-                  c);
-      const int rr = r & (kQRows - 1);
-      *reinterpret_cast<uint4*>(q_s + (r / kQRows) * kTile + (c >> 3) * kHalf + rr * 128 +
-                                (((c & 7) ^ (rr & 7)) << 4)) = v;
-    }
-    if (p.depth)
-      for (int i = tid - 128; i <= p.M; i += 256) sh->depth[i] = __ldg(p.depth + (int64_t)b * (p.M + 1) + i);
-    fence_async_smem();
-  }
-  __syncthreads();
+  // Ring order of an item's tiles: K_0 (and K_1 where the pipes take turns), then
+  // V_j, K_{j + la} in turn.  Key tiles are taken from the last to the first: with
+  // a bias by distance the largest scores come first, and the reference seldom
+  // moves.
+  auto k_idx = [](const Item& it, int j) {
+    const int la = it.dual ? 1 : 2;
+    return j < la ? j : 2 * j - la + 1;
+  };
+  auto v_idx = [](const Item& it, int j) { return j + min((it.dual ? 1 : 2) + j, it.nt); };
 
-  if (producer) {
-    // ---------------------------------------------------------------- K and V streams
-    bool to = false;
-    for (; issued < nt; ++issued) {
-      const int idx = is_k ? k_idx(issued) : v_idx(issued);
-      if (idx >= kSlots && !mbar_wait(&sh->empty[idx % kSlots], ((idx / kSlots) - 1) & 1, lim)) {
-        to = true;
-        break;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 3) {
+      // -------------------------------------------------------------- items
+      for (int n = 1;; ++n) {
+        const Item it = decode(blockIdx.x + n * gridDim.x, false);
+        if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sh->item_empty[n & 1], ((n >> 1) - 1) & 1))) break;
+        if (lane == 0) {
+          sh->item[n & 1] = it;
+          mbar_arrive(&sh->item_full[n & 1]);
+        }
+        __syncwarp();
+        if (it.index < 0) break;
       }
-      load(is_k ? &tmk : &tmv, idx, issued);
-    }
-    if (to) atomicExch(&sh->timed_out, 1);
-  } else if (warp == 1 && lane == 0 && nt > 0) {
-    // ---------------------------------------------------------------- MMA issue
-    const uint32_t idesc_s = idesc_bf16(128, kKeys, 0), idesc_o = idesc_bf16(128, D, 1);
-    const int n0 = dual ? nt : (nt + 1) / 2, n1 = dual ? nt : nt / 2;  // steps of the pipes
-    auto qk = [&](int q, int i) -> bool {
-      const int idx = k_idx(dual ? i : 2 * i + q), s = idx % kSlots;
-      if (!mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim)) return false;
-      tc_fence_after();
-      const uint64_t da = sw128_desc(smem_u32(q_s + (dual ? q : 0) * kTile), 16);
-      const uint64_t db = sw128_desc(smem_u32(ring + s * kTile), 16);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint64_t off = (uint64_t)((k >> 2) * (kHalf / 16) + (k & 3) * 2);
-        mma_ss(tmem + q * 256, da + off, db + off, idesc_s, k > 0 ? 1u : 0u);
+    } else if (warp != 1 && lane == 0) {
+      // -------------------------------------------------------------- K and V streams
+      const bool is_k = warp == 0;
+      const CUtensorMap* map = is_k ? &tmk : &tmv;
+      uint32_t base = 0;  // ring entries of earlier items
+      bool failed = false;
+      uint32_t end = 0;  // behind the last entry requested, to drain after a failure
+      for (int n = 0;; ++n) {
+        const Item it = next_item(n);
+        if (it.index < 0) break;
+        mbar_arrive(&sh->item_empty[n & 1]);
+        const int zc = it.sl * p.Hkv + it.hk;
+        for (int j = 0; j < it.nt && !failed; ++j) {
+          const uint32_t idx = base + (uint32_t)(is_k ? k_idx(it, j) : v_idx(it, j));
+          const uint32_t s = idx % kSlots;
+          if (idx >= (uint32_t)kSlots && !mbar_wait(&sh->empty[s], ((idx / kSlots) - 1) & 1, lim)) {
+            failed = true;
+            break;
+          }
+          mbar_arrive_expect_tx(&sh->full[s], kTile);
+          const int row = it.row0 + (it.nt - 1 - j) * kKeys;
+          if (D == 128)
+            tma_load_4d(ring + s * kTile, map, &sh->full[s], 0, row, 0, zc);
+          else
+            tma_load_3d(ring + s * kTile, map, &sh->full[s], 0, row, zc);
+          end = idx + 1;
+        }
+        if (failed) atomicExch(&sh->failed, 1);
+        base += 2 * it.nt;
       }
-      tc_commit(&sh->s_full[q]);
-      if (!dual || q == 1) tc_commit(&sh->empty[s]);
-      return true;
-    };
-    auto pv = [&](int q, int i, int n) -> bool {
-      const int idx = v_idx(dual ? i : 2 * i + q), s = idx % kSlots;
-      if (!mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim)) return false;
-      if (!mbar_wait(&sh->p_full[q], i & 1, lim)) return false;
-      tc_fence_after();
-      const uint64_t db = sw128_desc(smem_u32(ring + s * kTile), kHalf);
+      // a copy that no MMA waited for must land before the shared memory is released
+      if (failed || *(volatile int*)&sh->failed)
+        for (int i = 0; i < kSlots; ++i) {
+          const uint32_t idx = end - 1 - i;
+          if (end > (uint32_t)i) mbar_wait(&sh->full[idx % kSlots], (idx / kSlots) & 1, 10 * 1000 * 1000);
+        }
+    } else if (warp == 1 && lane == 0) {
+      // -------------------------------------------------------------- MMA issue
+      const uint32_t idesc_s = idesc_bf16(128, kKeys, 0), idesc_o = idesc_bf16(128, D, 1);
+      uint32_t base = 0, step0[2] = {0, 0};  // ring entries and steps of earlier items
+      uint32_t busy = 0;                     // items with work so far
+      bool ok = true;
+      for (int n = 0;; ++n) {
+        const Item it = next_item(n);
+        if (it.index < 0) break;
+        mbar_arrive(&sh->item_empty[n & 1]);
+        if (it.nt == 0 || !ok) continue;
+        const bool dual = it.dual;
+        const int n0 = dual ? it.nt : (it.nt + 1) / 2, n1 = dual ? it.nt : it.nt / 2;  // steps of the pipes
+        auto qk = [&](int q, int i) -> bool {
+          const uint32_t idx = base + k_idx(it, dual ? i : 2 * i + q), s = idx % kSlots;
+          if (!mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim)) return false;
+          tc_fence_after();
+          const uint64_t da = sw128_desc(smem_u32(q_s + (dual ? q : 0) * kTile), 16);
+          const uint64_t db = sw128_desc(smem_u32(ring + s * kTile), 16);
 #pragma unroll
-      for (int k = 0; k < kKeys / 16; ++k)
-        mma_ts(tmem + q * 256 + 128, tmem + q * 256 + k * 8, db + (uint64_t)(k * (16 * 128 / 16)), idesc_o,
-               (i > 0 || k > 0) ? 1u : 0u);
-      if (!dual || q == 1) tc_commit(&sh->empty[s]);
-      if (i == n - 1) tc_commit(&sh->o_full[q]);
-      return true;
-    };
-    bool ok = qk(0, 0);
-    if (ok && n1 > 0) ok = qk(1, 0);
-    for (int i = 0; i < n0 && ok; ++i) {
-      ok = pv(0, i, n0);
-      if (ok && i + 1 < n0) ok = qk(0, i + 1);
-      if (ok && i < n1) ok = pv(1, i, n1);
-      if (ok && i + 1 < n1) ok = qk(1, i + 1);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = (uint64_t)((k >> 2) * (kHalf / 16) + (k & 3) * 2);
+            mma_ss(tmem + q * 256, da + off, db + off, idesc_s, k > 0 ? 1u : 0u);
+          }
+          tc_commit(&sh->s_full[q]);
+          if (!dual || q == 1) tc_commit(&sh->empty[s]);
+          return true;
+        };
+        auto pv = [&](int q, int i, int steps) -> bool {
+          const uint32_t idx = base + v_idx(it, dual ? i : 2 * i + q), s = idx % kSlots;
+          if (!mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim)) return false;
+          if (!mbar_wait(&sh->p_full[q], (step0[q] + i) & 1, lim)) return false;
+          tc_fence_after();
+          const uint64_t db = sw128_desc(smem_u32(ring + s * kTile), kHalf);
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_ts(tmem + q * 256 + 128, tmem + q * 256 + k * 8, db + (uint64_t)(k * (16 * 128 / 16)), idesc_o,
+                   (i > 0 || k > 0) ? 1u : 0u);
+          if (!dual || q == 1) tc_commit(&sh->empty[s]);
+          if (i == steps - 1) tc_commit(&sh->o_full[q]);
+          return true;
+        };
+        ok = mbar_wait(&sh->q_full, busy & 1, lim);
+        ok = ok && qk(0, 0);
+        if (ok && n1 > 0) ok = qk(1, 0);
+        for (int i = 0; i < n0 && ok; ++i) {
+          ok = pv(0, i, n0);
+          if (ok && i + 1 < n0) ok = qk(0, i + 1);
+          if (ok && i < n1) ok = pv(1, i, n1);
+          if (ok && i + 1 < n1) ok = qk(1, i + 1);
+        }
+        if (!ok) atomicExch(&sh->failed, 1);
+        ++busy;
+        base += 2 * it.nt;
+        step0[0] += n0;
+        step0[1] += n1;
+      }
+      // every MMA issued retires before TMEM and shared memory are released
+      tc_commit(&sh->drain);
+      mbar_wait(&sh->drain, 0);
     }
-    if (!ok) atomicExch(&sh->timed_out, 1);
-    // every MMA issued retires before TMEM and shared memory are released
-    tc_commit(&sh->drain);
-    mbar_wait(&sh->drain, 0);
-  } else if (warp >= 4) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------------------------------------------------------- softmax
     const int pipe = (warp - 4) >> 2;
     const int r = (warp & 3) * 32 + lane;
-    const int qt = dual ? qt0 + pipe : qt0;
+    const uint32_t t_s = tmem + pipe * 256 + ((uint32_t)((warp & 3) * 32) << 16), t_o = t_s + 128;
+    uint32_t base = 0, step0 = 0, done_o[2] = {0, 0};  // ring entries, steps, finished O's of earlier items
+    bool to = false;  // a wait ran out: zero rows from here on
+    for (int n_item = 0;; ++n_item) {
+    const Item g = next_item(n_item);
+    if (g.index < 0) break;
+    const bool dual = g.dual;
+    const int nt = g.nt, hk = g.hk, b = g.b;
+    const int qt = dual ? g.qt0 + pipe : g.qt0;
+    if (nt > 0) {  // query rows -> swizzled shared memory; the tree rows' depths
+      // A thread brings one 16-byte column of every 16th (D = 128) or 32nd row, eight
+      // requests at a time.
+      constexpr int kC = D / 8, kStep = 256 / kC;
+      const int c = (tid - 128) % kC;
+#pragma unroll 1
+      for (int row0 = (tid - 128) / kC; row0 < (dual ? 2 : 1) * kQRows; row0 += 8 * kStep) {
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int gr = g.qt0 * kQRows + row0 + k * kStep;
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (gr < p.rows) v[k] = __ldg(reinterpret_cast<const uint4*>(p.q + query_row(p, b, hk, gr) * D) + c);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = row0 + k * kStep, rr = row & (kQRows - 1);
+          *reinterpret_cast<uint4*>(q_s + (row / kQRows) * kTile + (c >> 3) * kHalf + rr * 128 +
+                                    (((c & 7) ^ (rr & 7)) << 4)) = v[k];
+        }
+      }
+      if (p.depth)
+        for (int i = tid - 128; i <= p.M; i += 256) sh->depth[i] = (uint8_t)__ldg(p.depth + (int64_t)b * (p.M + 1) + i);
+      fence_async_smem();
+      tc_fence_before();
+      asm volatile("bar.sync 3, 256;" ::: "memory");
+      if (lane == 0) mbar_arrive(&sh->q_full);
+    }
     const int gr = qt * kQRows + r;
     const bool row_ok = gr < p.rows;
     const bool warp_live = __any_sync(0xffffffffu, row_ok);
-    const int u = min(gr / p.G, p.M);
+    const int u = min(node_of(p, min(gr, p.rows - 1)), p.M);
     const int64_t node = (int64_t)b * (p.M + 1) + u;
     const int du = (p.window > 0 || BIAS) && nt > 0 ? sh->depth[u] : 0;
-    const float slope2 = BIAS ? __ldg(p.slopes + hk * p.G + gr % p.G) * 1.4426950408889634f : 0.f;
+    const float slope2 =
+        BIAS ? __ldg(p.slopes + hk * p.G + (row_ok ? gr - u * p.G : 0)) * 1.4426950408889634f : 0.f;
     const int pos = g.kl + du;
     const int lo = p.window > 0 ? max(0, pos - (p.window - 1)) : 0;  // first prefix key of the row
-    const uint32_t t_s = tmem + pipe * 256 + ((uint32_t)((warp & 3) * 32) << 16), t_o = t_s + 128;
     const int n = dual ? nt : (pipe == 0 ? (nt + 1) / 2 : nt / 2);
     float m = TRACK ? -INFINITY : p.ref, l = 0.f;
     uint64_t l2[2] = {0ull, 0ull};
-    bool to = false;
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < n && !to; ++i) {
       const int j = dual ? i : 2 * i + pipe;
-      if (!__all_sync(0xffffffffu, mbar_wait(&sh->s_full[pipe], i & 1, lim))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh->s_full[pipe], (step0 + i) & 1, lim))) {
         to = true;
         break;
       }
       tc_fence_after();
       if (warp_live) {
-        const int key0 = g.first + (t0 + nt - 1 - j) * kKeys;  // of the sequence
+        const int key0 = g.first + (nt - 1 - j) * kKeys;  // of the sequence
         const bool edge = __any_sync(0xffffffffu, key0 + kKeys > g.kl || key0 < lo);
         bool done = false;
         // A tile inside the prefix, in one pass over S with the reference at hand;
@@ -526,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (p.window > 0)
                 for (uint32_t s = t; s; s &= s - 1) {
                   const int bit = __ffs(s) - 1;
-                  if (du - sh->depth[r0 + bit] >= p.window) t &= ~(1u << bit);
+                  if (du - (int)sh->depth[r0 + bit] >= p.window) t &= ~(1u << bit);
                 }
               w |= t;
             }
@@ -551,8 +642,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // The reference follows the maximum lazily: O is rescaled (a TMEM access of
             // the whole warp, each row by its own factor) only when some row's maximum
-            // has grown by more than 2^kGrow.  A full S says that O is not in use.
-            const bool grow = mx > m + kGrow;
+            // has grown by more than 2^kGrow; then every row's follows.  A full S says
+            // that O is not in use.
+            const bool grow = __any_sync(0xffffffffu, mx > m + kGrow) ? mx > m : false;
             const bool scale_o = grow && m != -INFINITY;
             if (__any_sync(0xffffffffu, scale_o)) {
               const float corr = scale_o ? fast_exp2(m - mx) : 1.f;
@@ -598,9 +690,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // V rows behind the step's may hold anything: zero them (the first pipe's
       // warps for both pipes where they share the tile; its PV is issued first)
-      const int kend = g.kl + p.M + 1 - (g.first + (t0 + nt - 1 - j) * kKeys);
+      const int kend = g.kl + p.M + 1 - (g.first + (nt - 1 - j) * kKeys);
       if (kend < kKeys && (!dual || pipe == 0)) {
-        const int idx = v_idx(j), s = idx % kSlots;
+        const uint32_t idx = base + v_idx(g, j), s = idx % kSlots;
         if (!__all_sync(0xffffffffu, mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim))) {
           to = true;
           break;
@@ -622,14 +714,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       f2_unpack(l2[1], s2, s3);
       l += (s0 + s1) + (s2 + s3);
     }
-    bool have = n > 0 && !to;
-    if (have && !mbar_wait(&sh->o_full[pipe], 0, lim)) to = true;
-    // (the second pipe's hand-over below goes through the ring: the first one's
-    // tiles must be used as well)
-    if (!dual && nt > 0 && !to && !mbar_wait(&sh->o_full[0], 0, lim)) to = true;
-    have = have && !to;
-    have = __all_sync(0xffffffffu, have);  // gates warp-collective TMEM reads
-    if (to) atomicExch(&sh->timed_out, 1);
+    if (n > 0 && !to && !mbar_wait(&sh->o_full[pipe], done_o[pipe] & 1, lim)) to = true;
+    // (the second pipe's hand-over below goes through the query tile, which the
+    // first one's products must have read)
+    if (!dual && nt > 0 && pipe == 1 && !to && !mbar_wait(&sh->o_full[0], done_o[0] & 1, lim)) to = true;
+    to = __any_sync(0xffffffffu, to);
+    const bool have = n > 0 && !to;
+    if (to && lane == 0) {
+      atomicExch(&sh->failed, 1);
+      atomicOr(&p.status[b], kSeqTimeout);
+    }
     tc_fence_after();
     if (!have) {
       m = -INFINITY;
@@ -637,9 +731,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // ---------------------------------------------------------------- epilogue
     // Pipes that shared a query tile join: the second hands its O, reference and
-    // sum to the first through the ring, whose tiles are all used.
-    float4* join_o = reinterpret_cast<float4*>(ring);                      // [D / 4][128]
-    float2* join_ml = reinterpret_cast<float2*>(ring + kQRows * D * 4);    // [128]
+    // sum to the first through the query tiles' memory.
+    float4* join_o = reinterpret_cast<float4*>(q_s);  // [D / 4][128]
     float w0 = 1.f, w1 = 0.f;
     if (!dual) {
       if (pipe == 1) {
@@ -659,11 +752,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
                             __uint_as_float(o[4 * e + 3]));
         }
-        join_ml[r] = make_float2(m, l);
+        sh->join_ml[r] = make_float2(m, l);
       }
       asm volatile("bar.sync 3, 256;" ::: "memory");
       if (pipe == 0) {
-        const float2 o = join_ml[r];
+        const float2 o = sh->join_ml[r];
         const float mm = fmaxf(m, o.x), ms = mm == -INFINITY ? 0.f : mm;
         w0 = fast_exp2(m - ms);  // 0 for a pipe without keys
         w1 = fast_exp2(o.x - ms);
@@ -672,13 +765,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (dual || pipe == 0) {
-      const bool whole = nr == 1;
+      const bool whole = g.nr == 1;
       const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
       w0 *= inv;
       w1 *= inv;
-      uint8_t* stage = q_s + pipe * kTile;  // this pipe's query tile is used: [128 rows][2 D bytes], chunks rotated
-      const int64_t rec = 2 * (int64_t)blockIdx.x + pipe;
+      uint8_t* stage = q_s + pipe * kTile;  // of a pair: this pipe's query tile, [128 rows][2 D bytes], chunks rotated
+      const int64_t rec = 2 * (int64_t)g.index + pipe;
       float4* dst = reinterpret_cast<float4*>(p.ws_o) + rec * (D / 4) * p.rec_rows;
+      uint4* out_row = reinterpret_cast<uint4*>(p.out + query_row(p, b, hk, min(gr, p.rows - 1)) * D);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -705,29 +799,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e) {
             const float4 x = a[2 * e], y = a[2 * e + 1];
             const int chunk = c * 4 + e;
-            *reinterpret_cast<uint4*>(stage + r * (2 * D) + ((chunk ^ (r & 7)) << 4)) =
-                make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+            const uint4 v = make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
+                                       pack_bf16x2(y.z, y.w));
+            if (dual)
+              *reinterpret_cast<uint4*>(stage + r * (2 * D) + ((chunk ^ (r & 7)) << 4)) = v;
+            else if (row_ok)
+              out_row[chunk] = v;
           }
         } else if (row_ok) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) __stcg(dst + (int64_t)(c * 8 + e) * p.rec_rows + r, a[e]);
         }
       }
-      if (whole) {
+      if (whole && dual) {
         asm volatile("bar.sync %0, 128;" ::"r"(1 + pipe) : "memory");
         const int rows = min(kQRows, p.rows - qt * kQRows);
-        const bool fail = *(volatile int*)&sh->timed_out != 0;
         for (int e = r; e < rows * (D / 8); e += kQRows) {
           const int rr = e / (D / 8), chunk = e % (D / 8);
-          const int g2 = qt * kQRows + rr;
-          uint4 v = *reinterpret_cast<const uint4*>(stage + rr * (2 * D) + ((chunk ^ (rr & 7)) << 4));
-          if (fail) v = make_uint4(0, 0, 0, 0);
-          reinterpret_cast<uint4*>(p.out + (((int64_t)b * (p.M + 1) + g2 / p.G) * p.Hq + hk * p.G + g2 % p.G) *
-                                               D)[chunk] = v;
+          reinterpret_cast<uint4*>(p.out + query_row(p, b, hk, qt * kQRows + rr) * D)[chunk] =
+              *reinterpret_cast<const uint4*>(stage + rr * (2 * D) + ((chunk ^ (rr & 7)) << 4));
         }
-      } else if (row_ok) {
+      } else if (!whole && row_ok) {
         __stcg(p.ws_ml + rec * p.rec_rows + r, make_float2(m, l));
       }
+    }
+    if (g.sl < 0 && tid == 128) atomicOr(&p.status[b], kSeqBadGeometry);
+    base += 2 * nt;
+    step0 += n;
+    if (nt > 0) ++done_o[0];
+    if (dual ? nt > 0 : nt > 1) ++done_o[1];
+    // the query tiles and depths are free for the next item
+    asm volatile("bar.sync 3, 256;" ::: "memory");
+    if (lane == 0) mbar_arrive(&sh->item_empty[n_item & 1]);
     }
   }
   tc_fence_before();
@@ -736,16 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // a copy that no MMA waited for must land before the shared memory is released
-  if (producer && sh->timed_out)
-    for (int j = max(0, issued - kSlots); j < issued; ++j) {
-      const int idx = is_k ? k_idx(j) : v_idx(j);
-      mbar_wait(&sh->full[idx % kSlots], (idx / kSlots) & 1);
-    }
-  if (tid == 0) {
-    const int flag = (sh->timed_out || !aligned_ok ? kSeqTimeout : 0) | (g.sl < 0 ? kSeqBadGeometry : 0);
-    if (flag) atomicOr(&p.status[b], flag);
-  }
+  if (!aligned_ok && tid == 0)
+    for (int b = 0; b < p.B; ++b) atomicOr(&p.status[b], kSeqTimeout);
 }
 
 // Joins the records of sequences whose key range was split: out = sum_i 2^(m_i -
@@ -755,8 +850,9 @@ __global__ void __launch_bounds__(256) scored_merge_kernel(const __grid_constant
   __shared__ int red[8];
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int qt = blockIdx.x % p.nqt, bh = blockIdx.x / p.nqt, hk = bh % p.Hkv, b = bh / p.Hkv;
   const int len = p.plan[0];
+  const float4* ws_o = reinterpret_cast<const float4*>(p.ws_o);
+  const int qt = blockIdx.x % p.nqt, hk = blockIdx.x / p.nqt % p.Hkv, b = blockIdx.x / p.nqt / p.Hkv;
   const int nr = ranges_of(sequence(p, b).nt, len);
   if (nr == 1) return;
   int before = 0;
@@ -771,7 +867,6 @@ __global__ void __launch_bounds__(256) scored_merge_kernel(const __grid_constant
   const int64_t item0 = ((int64_t)before * p.Hkv + (int64_t)hk * nr) * p.npairs + qt / 2;
   const int pipe = qt & 1;
   const bool fail = p.status[b] != 0;
-  const float4* ws_o = reinterpret_cast<const float4*>(p.ws_o);
   for (int e = blockIdx.y * 256 + threadIdx.x; e < rows * (D / 4); e += gridDim.y * 256) {
     const int r = e % rows, c = e / rows;
     float m = -INFINITY, l = 0.f;
@@ -806,13 +901,11 @@ __global__ void __launch_bounds__(256) scored_merge_kernel(const __grid_constant
       m = mm;
     }
     const float inv = !fail && l > 0.f ? 1.f / l : 0.f;
-    const int g2 = qt * kQRows + r;
     uint2 v = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
     if (fail) v = make_uint2(0u, 0u);
-    *reinterpret_cast<uint2*>(p.out + (((int64_t)b * (p.M + 1) + g2 / p.G) * p.Hq + hk * p.G + g2 % p.G) * D + 4 * c) =
-        v;
+    *reinterpret_cast<uint2*>(p.out + query_row(p, b, hk, qt * kQRows + r) * D + 4 * c) = v;
   }
-}
+  }
 
 // [BH][S_cap][D] bf16 in boxes of 128 rows: 64 columns (D = 64), or both 64-column
 // halves of a row (D = 128), landing as [half][row][128 B], 128-byte swizzle.
@@ -838,7 +931,7 @@ bool encode_scored_map(CUtensorMap* map, const void* base, int64_t BH, int64_t S
 
 // Grid and workspace of a shape (lengths are known on the device only).
 struct ScoredPlan {
-  int64_t grid;
+  int64_t grid, max_items;
   int sms, nqt, npairs, split, cand_step, rec_rows;
   size_t ml_off, ws_bytes;  // plan word, records, (reference, sum) pairs
 };
@@ -857,12 +950,12 @@ tv_status plan_scored(int B, int M, int Hq, int Hkv, int D, int64_t S_cap, int w
   int64_t keys = std::max<int64_t>(S_cap, 1);
   if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window - 1 + M + 1);
   const int64_t tiles = (keys + kKeys - 1) / kKeys;
-  // Ranges are split while the items stay below kMaxRounds rounds of the SMs: shorter
-  // items would balance the SMs further, but their set-up and merge cost more.
+  // Ranges are split while the sequences give fewer than kMaxRounds items per SM.
   lp.split = base < kMaxRounds * (int64_t)lp.sms && tiles >= 2 * kMinSplitTiles && tiles < (1 << 20);
-  lp.grid = lp.split ? kMaxRounds * (int64_t)lp.sms : base;
+  lp.max_items = lp.split ? kMaxRounds * (int64_t)lp.sms : base;
+  lp.grid = std::min<int64_t>(lp.max_items, lp.sms);
   lp.cand_step = (int)((tiles + kThreads - kMinSplitTiles - 2) / (kThreads - kMinSplitTiles - 1));
-  const size_t recs = lp.split ? 2 * (size_t)lp.grid * lp.rec_rows : 0;
+  const size_t recs = lp.split ? 2 * (size_t)lp.max_items * lp.rec_rows : 0;
   lp.ml_off = 256 + recs * D * sizeof(float);
   lp.ws_bytes = lp.split ? lp.ml_off + recs * sizeof(float2) : 0;
   return TV_OK;
@@ -881,9 +974,10 @@ tv_status launch_scored(int mode, const CUtensorMap& tmk, const CUtensorMap& tmv
   if (e != cudaSuccess) return record_cuda_error(e);
   tv_status r = launch(kern, dim3((unsigned)lp.grid), dim3(kThreads), smem, s, 1, true, tmk, tmv, p);
   if (r != TV_OK || !lp.split) return r;
-  const int per_tile = (lp.rec_rows * (D / 4) + 255) / 256;
-  return launch(scored_merge_kernel<D>, dim3((unsigned)((int64_t)p.B * p.Hkv * p.nqt), per_tile), dim3(256), 0, s, 1,
-                true, p);
+  // about four blocks an SM (at most 16 have work per unit): most find a sequence in one range and leave
+  const int units = p.B * p.Hkv * p.nqt;
+  const int parts = std::max(1, std::min((lp.rec_rows * (D / 4) + 255) / 256, 4 * lp.sms / units));
+  return launch(scored_merge_kernel<D>, dim3(units, parts), dim3(256), 0, s, 1, true, p);
 }
 
 }  // namespace
@@ -893,7 +987,7 @@ extern "C" size_t tree_attention_scored_workspace_size(int B, int M, int Hq, int
                                                        int window) {
   using namespace tv;
   if (B <= 0 || M < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128) || M + 1 > kMaxRows ||
-      S_cap < 0 || window < 0 || (int64_t)(Hq / Hkv) * (M + 1) > (1 << 24))
+      S_cap < 0 || window < 0 || (int64_t)(Hq / Hkv) * (M + 1) >= (1 << 21))
     return 0;
   ScoredPlan lp;
   return plan_scored(B, M, Hq, Hkv, D, S_cap, window, lp) == TV_OK ? lp.ws_bytes : 0;
@@ -913,7 +1007,7 @@ extern "C" tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k,
   if (M + 1 > kMaxRows || S_cap > 0x7fffffffLL || B > kMaxBatch) return TV_ERR_UNSUPPORTED;
   // the polynomial's coefficients hold (scale / softcap)^8
   if (softcap > 0.f && scale / softcap > 1e4f) return TV_ERR_UNSUPPORTED;
-  if ((int64_t)(Hq / Hkv) * (M + 1) > (1 << 24)) return TV_ERR_UNSUPPORTED;
+  if ((int64_t)(Hq / Hkv) * (M + 1) >= (1 << 21)) return TV_ERR_UNSUPPORTED;
   if (B == 0) return TV_OK;
   if (!q || !k || !v || !kv_start || !kv_len || !anc_mask || !status || !out) return TV_ERR_INVALID_ARG;
   if ((window > 0 || alibi_slopes) && !depth) return TV_ERR_INVALID_ARG;
@@ -921,7 +1015,7 @@ extern "C" tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k,
   ScoredPlan lp;
   tv_status r = plan_scored(B, M, Hq, Hkv, D, S_cap, window, lp);
   if (r != TV_OK) return r;
-  if (lp.grid > 0x3fffffffLL || (int64_t)B * Hkv * lp.nqt > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
+  if (lp.max_items > 0x3fffffffLL || (int64_t)B * Hkv * lp.nqt > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
   if (lp.ws_bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < lp.ws_bytes))
     return TV_ERR_INVALID_ARG;
   ScoredParams p = {};
@@ -943,11 +1037,12 @@ extern "C" tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k,
   p.W = (M + 1 + 31) / 32;
   p.n_slots = slot ? n_slots : B;
   p.window = window;
+  p.inv_g = 1.f / (float)p.G;
   p.rows = p.G * (M + 1);
   p.nqt = lp.nqt;
   p.npairs = lp.npairs;
   p.rec_rows = lp.rec_rows;
-  p.sms = lp.sms;
+  p.max_items = lp.max_items;
   p.split = lp.split;
   p.cand_step = lp.cand_step;
   const double log2e = 1.4426950408889634;
