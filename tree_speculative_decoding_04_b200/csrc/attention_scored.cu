@@ -14,20 +14,26 @@
 //   out = sum_x 2^(s - r) v_x / sum_x 2^(s - r)     for any reference r
 //
 // Work.  The G (M+1) query rows of a (sequence, kv head) form tiles of 128, the
-// keys it can see (from the root's window on) tiles of 128.  A CTA takes an
+// keys it can see (from the root's window on) tiles of 80.  A CTA takes an
 // item: two query tiles and a range of key tiles.  Each of its two pipes (a
 // softmax warpgroup with a TMEM block of its own) owns one query tile and both
 // read every K/V tile; where only one query tile is left, the pipes share it
 // and take the even and the odd key tiles.  While one pipe's softmax runs, the
 // tensor core works for the other.
 //
-// Warps (384 threads, one CTA per SM): 0 requests K tiles, 2 V tiles, both into
-// one ring of slots in the order the MMAs use them; 1 issues the MMAs
-//   S_q  = Q K^T    M = 128, N = 128, A and B from shared memory -> TMEM
-//   O_q += P_q V    M = 128, N = D,   A = P from TMEM, V from shared memory
-// 4-7 and 8-11 are the pipes' softmax warps: thread t owns TMEM lane t, one
-// query row, and writes P over its scores.  QK_q of the next tile is issued
-// behind PV_q of this one, so a full S_q also says that PV_q is done.
+// Warps (384 threads, one CTA per SM, kept for several items):
+//   0     requests K and V tiles into one ring of slots in the order of their use
+//   1     TMEM owner; works out the CTA's next item one ahead
+//   2, 3  issue the MMAs of a pipe each:
+//           S = Q K^T   M = 128, N = 80, A and B from shared memory -> TMEM
+//           O += P V    M = 128, N = D,  A = P from TMEM, V from shared memory
+//   4-11  the pipes' softmax warps: thread t owns TMEM lane t, one query row
+// TMEM columns of a pipe: S [0, 80), P [80, 120), O [128, 128 + D).  Tiles of 80
+// keys leave P columns of its own beside S, so the next S is formed while the
+// softmax still works on this one.  (Tiles of 128 keys with P written over S: PV
+// and the next QK lay between two softmax phases of a pipe, 1.0 us after 1.1-1.4
+// us of softmax; 128 query rows x 64 heads x 8 sequences of 4096-16384 keys took
+// 551 us.)
 #include <algorithm>
 #include <climits>
 
@@ -38,18 +44,21 @@ namespace tv {
 namespace {
 
 constexpr int kQRows = 128;
-constexpr int kKeys = 128;                 // keys per tile
-constexpr int kHalf = kKeys * 128;         // one 64-column half of a tile: 128 rows x 128 B
-constexpr int kRingBytes = 163840;
-constexpr int kMaxSlots = 10;
+constexpr int kKeys = 80;                  // keys per tile
+constexpr int kHalf = kKeys * 128;         // one 64-column half of a K or V tile: 80 rows x 128 B
+constexpr int kQHalf = kQRows * 128;       // of a query tile
+constexpr int kRingBytes = 14 * kHalf;
+constexpr int kMaxSlots = 14;
 constexpr int kThreads = 384;
+// TMEM columns of a pipe's 256
+constexpr int kColP = kKeys, kColO = 128;
 // A row's reference moves once a score lies more than 2^kGrow above it (the
 // weights are floats in bf16 and sums in fp32: a large weight is as exact as a
 // small one, and 2^24 leaves both far from their limits).
 constexpr float kGrow = 24.0f;
-constexpr int kMaxBatch = 16384;
+constexpr int kMaxBatch = 4096;
 constexpr int kMaxRounds = 6;              // items per SM, at most, where ranges are split
-constexpr int kMinSplitTiles = 4;          // key tiles below which a range is not split further
+constexpr int kMinSplitTiles = 6;          // key tiles below which a range is not split further
 constexpr int kMaxRankedRows = kThreads;
 
 // Which scores an instance computes.
@@ -122,7 +131,7 @@ struct Item {
 
 struct Shared {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t s_full[2], p_full[2], o_full[2], q_full;
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full;
   uint64_t item_full[2], item_empty[2];
   uint64_t drain;
   unsigned long long best;
@@ -132,9 +141,10 @@ struct Shared {
   float2 join_ml[kQRows];
   uint16_t order[kMaxRankedRows];
   uint8_t depth[kMaxRows];
+  uint32_t anc[2 * kQRows][kMaxRows / 32 + 1];  // ancestor words of the softmax threads' rows
 };
-constexpr int kItemReaders = 3 + 8;  // both producers, the MMA thread, the softmax warps
-static_assert(4 * kHalf + kRingBytes + sizeof(Shared) <= 232448, "shared memory of a CTA");
+constexpr int kItemReaders = 3 + 8;  // the producer warp, both MMA threads, the softmax warps
+static_assert(4 * kQHalf + kRingBytes + sizeof(Shared) <= 232448, "shared memory of a CTA");
 
 // Row of q and out ([B][M+1][Hq]) of the gr-th query row of (b, hk).  gr / G by a
 // reciprocal: exact for G (M+1) < 2^21, which the host checks.
@@ -153,32 +163,32 @@ __device__ __forceinline__ float cap_score(float x, const ScoredParams& p) {
   return fabsf(x) <= p.x_lim ? x * g : p.cap_log2 * (1.f - __fdividef(2.f, fast_exp2(x * p.z2) + 1.f));
 }
 
-// 32 scores of a row, minus `sub`, from the raw products x of keys kc .. kc+31, in
+// 16 scores of a row, minus `sub`, from the raw products x of keys kc .. kc+15, in
 // the general form.  ok: the keys that count (used where `edge`; what lies behind
 // the step's rows may be anything).  slope2, pos: the row's bias per position
 // (log2) and its position; dep: the tree rows' depths.
 template <int MODE>
-__device__ __forceinline__ void chunk_scores(float (&x)[32], const ScoredParams& p, bool edge, uint32_t ok, float sub,
+__device__ __forceinline__ void chunk_scores(float (&x)[16], const ScoredParams& p, bool edge, uint32_t ok, float sub,
                                              float slope2, int pos, int kc, int kl, int du, const uint8_t* dep) {
   constexpr bool CAP = MODE == kCapLow || MODE == kCapHigh || MODE == kCapBias;
   constexpr bool BIAS = MODE == kBias || MODE == kCapBias;
   if (edge) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] = (ok >> j) & 1u ? x[j] : 0.f;
+    for (int j = 0; j < 16; ++j) x[j] = (ok >> j) & 1u ? x[j] : 0.f;
   }
   bool far = false;
   if (CAP) {
     float a[2] = {fabsf(x[0]), fabsf(x[1])};
 #pragma unroll
-    for (int j = 2; j < 32; j += 2) a[(j >> 1) & 1] = fmax3(a[(j >> 1) & 1], fabsf(x[j]), fabsf(x[j + 1]));
+    for (int j = 2; j < 16; j += 2) a[(j >> 1) & 1] = fmax3(a[(j >> 1) & 1], fabsf(x[j]), fabsf(x[j + 1]));
     far = __any_sync(0xffffffffu, fmaxf(a[0], a[1]) > p.x_lim);
   }
   if (far) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] = cap_score(x[j], p);
+    for (int j = 0; j < 16; ++j) x[j] = cap_score(x[j], p);
   } else {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const uint64_t v = f2_pack(x[2 * j], x[2 * j + 1]);
       uint64_t g = f2_pack(p.scale_log2, p.scale_log2);
       if (CAP) {
@@ -190,20 +200,20 @@ __device__ __forceinline__ void chunk_scores(float (&x)[32], const ScoredParams&
       f2_unpack(f2_mul(v, g), x[2 * j], x[2 * j + 1]);
     }
   }
-  if (BIAS && kc + 32 > kl) {
+  if (BIAS && kc + 16 > kl) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
+    for (int j = 0; j < 16; ++j) {
       const int t = kc + j - kl;  // tree row
       const int dist = t < 0 ? pos - (kc + j) : du - (int)dep[min(t, p.M)];
       x[j] += fmaf(-slope2, (float)dist, -sub);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] += BIAS ? fmaf(-slope2, (float)(pos - (kc + j)), -sub) : -sub;
+    for (int j = 0; j < 16; ++j) x[j] += BIAS ? fmaf(-slope2, (float)(pos - (kc + j)), -sub) : -sub;
   }
   if (edge) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] = (ok >> j) & 1u ? x[j] : -INFINITY;
+    for (int j = 0; j < 16; ++j) x[j] = (ok >> j) & 1u ? x[j] : -INFINITY;
   }
 }
 
@@ -215,12 +225,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool CAP = MODE == kCapLow || MODE == kCapHigh || MODE == kCapBias;
   constexpr bool TRACK = MODE != kCapLow;  // a running maximum is kept
   constexpr int kHalves = D / 64;
-  constexpr int kTile = kHalves * kHalf;  // K, V or Q tile
+  constexpr int kTile = kHalves * kHalf;   // K or V tile
+  constexpr int kQTile = kHalves * kQHalf;
   constexpr int kSlots = kRingBytes / kTile;
   static_assert(kSlots <= kMaxSlots, "ring");
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* q_s = smem;               // [2][halves][128][128 B]
-  uint8_t* ring = smem + 2 * kTile;  // [slots][halves][128][128 B]
+  uint8_t* q_s = smem;                // [2][halves][128][128 B]
+  uint8_t* ring = smem + 2 * kQTile;  // [slots][halves][80][128 B]
   Shared* sh = reinterpret_cast<Shared*>(ring + kRingBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -229,19 +240,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh->best = ~0ull;
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], 1);
+      mbar_init(&sh->empty[s], 2);
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(&sh->s_full[q], 1);
+      mbar_init(&sh->s_free[q], 4);
       mbar_init(&sh->p_full[q], 4);
-      mbar_init(&sh->o_full[q], 1);
+      mbar_init(&sh->pv_done[q], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->item_full[i], 1);
       mbar_init(&sh->item_empty[i], kItemReaders);
     }
     mbar_init(&sh->q_full, 8);
-    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->drain, 2);
     fence_mbar_init();
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
@@ -257,10 +269,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---------------------------------------------------------------- the plan
   // Every CTA forms the same plan from the sequences' lengths: the number of key
   // tiles per range that finishes first by this estimate, in steps of a pipe
-  // pair: the items of a CTA one after another, 2 steps of set-up and epilogue
-  // each, 3 for the merge where ranges are split.  Each thread tries one length.
+  // pair: the items of a CTA one after another, 4 steps of set-up and epilogue
+  // each, 4 for the merge where ranges are split.  Each thread tries one length.
   int* nt_s = reinterpret_cast<int*>(ring);
-  for (int b = tid; b < p.B; b += kThreads) nt_s[b] = sequence(p, b).nt;
+  int4* geo_s = reinterpret_cast<int4*>(ring + 4 * kMaxBatch);
+  for (int b = tid; b < p.B; b += kThreads) {
+    const int st = __ldcg(p.status + b);
+    const Geo g = sequence(p, b);
+    nt_s[b] = g.nt;
+    geo_s[b] = make_int4(g.sl, g.ks, g.kl, st);
+  }
   __syncthreads();
   int len = INT_MAX;
   const int per_range = p.Hkv * p.npairs;  // items of one key range of a sequence
@@ -278,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t rounds = (items + gridDim.x - 1) / gridDim.x;
       // a lone query tile takes half the steps of a pair
       const int64_t mean = (ranges * p.Hkv * p.nqt * l) / (2 * gridDim.x);
-      const int64_t est = min(rounds * steps, mean + steps) + 2 * rounds + (ranges > p.B ? 3 : 0);
+      const int64_t est = min(rounds * steps, mean + steps) + 4 * rounds + (ranges > p.B ? 4 : 0);
       key = (unsigned long long)est << 32 | (uint32_t)~l;  // the longest of equal ones
     }
 #pragma unroll
@@ -298,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  // Item `index`, by warp 3; the first one reads the plan's scratch.
+  // Item `index`, by warp 1; the first one reads the plan's scratch.
   const bool aligned_ok = (smem_u32(smem) & 1023u) == 0;  // the swizzled tiles need it (else all sequences fail)
   auto decode = [&](int index, bool scratch) -> Item {
     Item it = {};
@@ -319,7 +337,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int src = __ffs(m) - 1;
         it.b = __shfl_sync(0xffffffffu, b, src);
         const int rem = index - __shfl_sync(0xffffffffu, base + incl - cnt, src);
-        const Geo g = sequence(p, it.b);
+        Geo g;
+        int st;
+        if (scratch) {
+          const int4 v = geo_s[it.b];
+          g = Geo{v.x, v.y, v.z, 0, nt_s[it.b]};
+          g.first = p.window > 0 ? max(0, g.kl - (p.window - 1)) : 0;
+          st = v.w;
+        } else {
+          g = sequence(p, it.b);
+          st = __ldcg(p.status + it.b);
+        }
         it.index = index;
         it.nr = ranges_of(g.nt, len);
         it.qt0 = 2 * (rem % p.npairs);
@@ -331,14 +359,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.kl = g.kl;
         it.first = g.first + range * per * kKeys;
         it.row0 = g.ks + it.first;
-        it.nt = aligned_ok && __ldcg(p.status + it.b) == 0 ? max(0, min(per, g.nt - range * per)) : 0;
+        it.nt = aligned_ok && st == 0 ? max(0, min(per, g.nt - range * per)) : 0;
         return it;
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
     return it;
   };
-  if (warp == 3) {
+  if (warp == 1) {
     const Item it = decode(blockIdx.x, true);
     if (lane == 0) sh->item[0] = it;
     __syncwarp();
@@ -369,8 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto v_idx = [](const Item& it, int j) { return j + min((it.dual ? 1 : 2) + j, it.nt); };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 3) {
+    if (warp == 1) {
       // -------------------------------------------------------------- items
       for (int n = 1;; ++n) {
         const Item it = decode(blockIdx.x + n * gridDim.x, false);
@@ -382,47 +409,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (it.index < 0) break;
       }
-    } else if (warp != 1 && lane == 0) {
-      // -------------------------------------------------------------- K and V streams
-      const bool is_k = warp == 0;
-      const CUtensorMap* map = is_k ? &tmk : &tmv;
-      uint32_t base = 0;  // ring entries of earlier items
+    } else if (warp == 0) {
+      // -------------------------------------------------------------- K and V stream
+      // The warp walks the ring; lane 0 requests K tiles, lane 1 V tiles (the copies
+      // one thread issues are processed one after another).
+      uint32_t idx = 0;  // ring entries so far
       bool failed = false;
-      uint32_t end = 0;  // behind the last entry requested, to drain after a failure
       for (int n = 0;; ++n) {
         const Item it = next_item(n);
         if (it.index < 0) break;
-        mbar_arrive(&sh->item_empty[n & 1]);
-        const int zc = it.sl * p.Hkv + it.hk;
-        for (int j = 0; j < it.nt && !failed; ++j) {
-          const uint32_t idx = base + (uint32_t)(is_k ? k_idx(it, j) : v_idx(it, j));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->item_empty[n & 1]);
+        const int zc = it.sl * p.Hkv + it.hk, la = it.dual ? 1 : 2;
+        for (int kj = 0, vj = 0; vj < it.nt && !failed; ++idx) {
           const uint32_t s = idx % kSlots;
-          if (idx >= (uint32_t)kSlots && !mbar_wait(&sh->empty[s], ((idx / kSlots) - 1) & 1, lim)) {
+          if (idx >= (uint32_t)kSlots &&
+              !__all_sync(0xffffffffu, mbar_wait(&sh->empty[s], ((idx / kSlots) - 1) & 1, lim))) {
             failed = true;
             break;
           }
-          mbar_arrive_expect_tx(&sh->full[s], kTile);
-          const int row = it.row0 + (it.nt - 1 - j) * kKeys;
-          if (D == 128)
-            tma_load_4d(ring + s * kTile, map, &sh->full[s], 0, row, 0, zc);
-          else
-            tma_load_3d(ring + s * kTile, map, &sh->full[s], 0, row, zc);
-          end = idx + 1;
+          const bool is_k = kj < it.nt && kj - vj < la;
+          const int j = is_k ? kj++ : vj++;
+          if (lane == (is_k ? 0 : 1)) {
+            const CUtensorMap* map = is_k ? &tmk : &tmv;
+            mbar_arrive_expect_tx(&sh->full[s], kTile);
+            const int row = it.row0 + (it.nt - 1 - j) * kKeys;
+            if (D == 128)
+              tma_load_4d(ring + s * kTile, map, &sh->full[s], 0, row, 0, zc);
+            else
+              tma_load_3d(ring + s * kTile, map, &sh->full[s], 0, row, zc);
+          }
+          __syncwarp();
         }
-        if (failed) atomicExch(&sh->failed, 1);
-        base += 2 * it.nt;
+        if (failed && lane == 0) atomicExch(&sh->failed, 1);
       }
       // a copy that no MMA waited for must land before the shared memory is released
-      if (failed || *(volatile int*)&sh->failed)
-        for (int i = 0; i < kSlots; ++i) {
-          const uint32_t idx = end - 1 - i;
-          if (end > (uint32_t)i) mbar_wait(&sh->full[idx % kSlots], (idx / kSlots) & 1, 10 * 1000 * 1000);
-        }
-    } else if (warp == 1 && lane == 0) {
-      // -------------------------------------------------------------- MMA issue
+      if (failed || __any_sync(0xffffffffu, *(volatile int*)&sh->failed))
+        for (uint32_t i = 1; i <= (uint32_t)kSlots && i <= idx; ++i)
+          mbar_wait(&sh->full[(idx - i) % kSlots], ((idx - i) / kSlots) & 1);
+    } else if (lane == 0) {
+      // -------------------------------------------------------------- MMA issue, one thread per pipe
+      const int q = warp - 2;
       const uint32_t idesc_s = idesc_bf16(128, kKeys, 0), idesc_o = idesc_bf16(128, D, 1);
-      uint32_t base = 0, step0[2] = {0, 0};  // ring entries and steps of earlier items
-      uint32_t busy = 0;                     // items with work so far
+      const uint32_t t_q = tmem + q * 256;
+      uint32_t base = 0, step0 = 0, busy = 0;  // ring entries, steps and items with work so far
       bool ok = true;
       for (int n = 0;; ++n) {
         const Item it = next_item(n);
@@ -430,62 +460,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sh->item_empty[n & 1]);
         if (it.nt == 0 || !ok) continue;
         const bool dual = it.dual;
-        const int n0 = dual ? it.nt : (it.nt + 1) / 2, n1 = dual ? it.nt : it.nt / 2;  // steps of the pipes
-        auto qk = [&](int q, int i) -> bool {
-          const uint32_t idx = base + k_idx(it, dual ? i : 2 * i + q), s = idx % kSlots;
+        const int steps = dual ? it.nt : (it.nt + 1 - q) / 2;
+        // a slot is free once both pipes have read it, or its one reader has
+        auto release = [&](uint32_t s) {
+          tc_commit(&sh->empty[s]);
+          if (!dual) tc_commit(&sh->empty[s]);
+        };
+        auto qk = [&](int i) -> bool {
+          const uint32_t idx = base + k_idx(it, dual ? i : 2 * i + q), s = idx % kSlots, st = step0 + i;
           if (!mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim)) return false;
+          if (st > 0 && !mbar_wait(&sh->s_free[q], (st - 1) & 1, lim)) return false;
           tc_fence_after();
-          const uint64_t da = sw128_desc(smem_u32(q_s + (dual ? q : 0) * kTile), 16);
+          const uint64_t da = sw128_desc(smem_u32(q_s + (dual ? q : 0) * kQTile), 16);
           const uint64_t db = sw128_desc(smem_u32(ring + s * kTile), 16);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = (uint64_t)((k >> 2) * (kHalf / 16) + (k & 3) * 2);
-            mma_ss(tmem + q * 256, da + off, db + off, idesc_s, k > 0 ? 1u : 0u);
-          }
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(t_q, da + (uint64_t)((k >> 2) * (kQHalf / 16) + (k & 3) * 2),
+                   db + (uint64_t)((k >> 2) * (kHalf / 16) + (k & 3) * 2), idesc_s, k > 0 ? 1u : 0u);
           tc_commit(&sh->s_full[q]);
-          if (!dual || q == 1) tc_commit(&sh->empty[s]);
+          release(s);
           return true;
         };
-        auto pv = [&](int q, int i, int steps) -> bool {
+        ok = mbar_wait(&sh->q_full, busy & 1, lim) && (steps == 0 || qk(0));
+        for (int i = 0; i < steps && ok; ++i) {
+          if (i + 1 < steps && !(ok = qk(i + 1))) break;
           const uint32_t idx = base + v_idx(it, dual ? i : 2 * i + q), s = idx % kSlots;
-          if (!mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim)) return false;
-          if (!mbar_wait(&sh->p_full[q], (step0[q] + i) & 1, lim)) return false;
+          ok = mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim) && mbar_wait(&sh->p_full[q], (step0 + i) & 1, lim);
+          if (!ok) break;
           tc_fence_after();
           const uint64_t db = sw128_desc(smem_u32(ring + s * kTile), kHalf);
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
-            mma_ts(tmem + q * 256 + 128, tmem + q * 256 + k * 8, db + (uint64_t)(k * (16 * 128 / 16)), idesc_o,
+            mma_ts(t_q + kColO, t_q + kColP + k * 8, db + (uint64_t)(k * (16 * 128 / 16)), idesc_o,
                    (i > 0 || k > 0) ? 1u : 0u);
-          if (!dual || q == 1) tc_commit(&sh->empty[s]);
-          if (i == steps - 1) tc_commit(&sh->o_full[q]);
-          return true;
-        };
-        ok = mbar_wait(&sh->q_full, busy & 1, lim);
-        ok = ok && qk(0, 0);
-        if (ok && n1 > 0) ok = qk(1, 0);
-        for (int i = 0; i < n0 && ok; ++i) {
-          ok = pv(0, i, n0);
-          if (ok && i + 1 < n0) ok = qk(0, i + 1);
-          if (ok && i < n1) ok = pv(1, i, n1);
-          if (ok && i + 1 < n1) ok = qk(1, i + 1);
+          tc_commit(&sh->pv_done[q]);
+          release(s);
         }
         if (!ok) atomicExch(&sh->failed, 1);
         ++busy;
         base += 2 * it.nt;
-        step0[0] += n0;
-        step0[1] += n1;
+        step0 += steps;
       }
       // every MMA issued retires before TMEM and shared memory are released
       tc_commit(&sh->drain);
       mbar_wait(&sh->drain, 0);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------------------------------------------------------- softmax
     const int pipe = (warp - 4) >> 2;
     const int r = (warp & 3) * 32 + lane;
-    const uint32_t t_s = tmem + pipe * 256 + ((uint32_t)((warp & 3) * 32) << 16), t_o = t_s + 128;
-    uint32_t base = 0, step0 = 0, done_o[2] = {0, 0};  // ring entries, steps, finished O's of earlier items
+    const int stid = tid - 128;  // of the 256 softmax threads
+    const uint32_t t_s = tmem + pipe * 256 + ((uint32_t)((warp & 3) * 32) << 16), t_p = t_s + kColP, t_o = t_s + kColO;
+    uint32_t base = 0, step0 = 0;  // ring entries and steps of earlier items
     bool to = false;  // a wait ran out: zero rows from here on
     for (int n_item = 0;; ++n_item) {
     const Item g = next_item(n_item);
@@ -493,39 +519,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool dual = g.dual;
     const int nt = g.nt, hk = g.hk, b = g.b;
     const int qt = dual ? g.qt0 + pipe : g.qt0;
+    const int gr = qt * kQRows + r;
+    const bool row_ok = gr < p.rows;
+    const bool warp_live = __any_sync(0xffffffffu, row_ok);
+    const int u = min(node_of(p, min(gr, p.rows - 1)), p.M);
     if (nt > 0) {  // query rows -> swizzled shared memory; the tree rows' depths
-      // A thread brings one 16-byte column of every 16th (D = 128) or 32nd row, eight
-      // requests at a time.
-      constexpr int kC = D / 8, kStep = 256 / kC;
-      const int c = (tid - 128) % kC;
-#pragma unroll 1
-      for (int row0 = (tid - 128) / kC; row0 < (dual ? 2 : 1) * kQRows; row0 += 8 * kStep) {
-        uint4 v[8];
+      // A thread brings one 16-byte column of every 16th (D = 128) or 32nd row, all
+      // its requests in flight at once.
+      constexpr int kC = D / 8, kStep = 256 / kC, kN = 2 * kQRows / kStep;
+      const int c = stid % kC, r0 = stid / kC;
+      uint4 v[kN];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int gr = g.qt0 * kQRows + row0 + k * kStep;
-          v[k] = make_uint4(0, 0, 0, 0);
-          if (gr < p.rows) v[k] = __ldg(reinterpret_cast<const uint4*>(p.q + query_row(p, b, hk, gr) * D) + c);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int row = row0 + k * kStep, rr = row & (kQRows - 1);
-          *reinterpret_cast<uint4*>(q_s + (row / kQRows) * kTile + (c >> 3) * kHalf + rr * 128 +
-                                    (((c & 7) ^ (rr & 7)) << 4)) = v[k];
-        }
+      for (int k = 0; k < kN; ++k) {
+        const int gr = g.qt0 * kQRows + r0 + k * kStep;
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (gr < p.rows && (dual || k < kN / 2))
+          v[k] = __ldg(reinterpret_cast<const uint4*>(p.q + query_row(p, b, hk, gr) * D) + c);
       }
+      for (int i = 0; i < p.W; ++i) sh->anc[stid][i] = __ldg(p.anc + ((int64_t)b * (p.M + 1) + u) * p.W + i);
       if (p.depth)
-        for (int i = tid - 128; i <= p.M; i += 256) sh->depth[i] = (uint8_t)__ldg(p.depth + (int64_t)b * (p.M + 1) + i);
+        for (int i = stid; i <= p.M; i += 256) sh->depth[i] = (uint8_t)__ldg(p.depth + (int64_t)b * (p.M + 1) + i);
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const int row = r0 + k * kStep, rr = row & (kQRows - 1);
+        if (dual || k < kN / 2)
+          *reinterpret_cast<uint4*>(q_s + (row / kQRows) * kQTile + (c >> 3) * kQHalf + rr * 128 +
+                                    (((c & 7) ^ (rr & 7)) << 4)) = v[k];
+      }
       fence_async_smem();
       tc_fence_before();
       asm volatile("bar.sync 3, 256;" ::: "memory");
       if (lane == 0) mbar_arrive(&sh->q_full);
     }
-    const int gr = qt * kQRows + r;
-    const bool row_ok = gr < p.rows;
-    const bool warp_live = __any_sync(0xffffffffu, row_ok);
-    const int u = min(node_of(p, min(gr, p.rows - 1)), p.M);
-    const int64_t node = (int64_t)b * (p.M + 1) + u;
     const int du = (p.window > 0 || BIAS) && nt > 0 ? sh->depth[u] : 0;
     const float slope2 =
         BIAS ? __ldg(p.slopes + hk * p.G + (row_ok ? gr - u * p.G : 0)) * 1.4426950408889634f : 0.f;
@@ -541,77 +566,123 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
+      const int key0 = g.first + (nt - 1 - j) * kKeys;  // of the sequence
+      // S is read: the next S may be formed while this one's weights are
+      auto free_s = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->s_free[pipe]);
+      };
+      // the products with the weights before these are done: P and O are free
+      auto wait_pv = [&]() -> bool {
+        if (i > 0 && !__all_sync(0xffffffffu, mbar_wait(&sh->pv_done[pipe], (step0 + i - 1) & 1, lim))) return false;
+        tc_fence_after();
+        return true;
+      };
+      bool s_kept = true;
       if (warp_live) {
-        const int key0 = g.first + (nt - 1 - j) * kKeys;  // of the sequence
         const bool edge = __any_sync(0xffffffffu, key0 + kKeys > g.kl || key0 < lo);
         bool done = false;
-        // A tile inside the prefix, in one pass over S with the reference at hand;
-        // the weights stay in registers until the warp knows that every score lay in
-        // the polynomial's range and below the reference's headroom.  S is still there
-        // for the general path if not.
-        if (!edge && (!TRACK || i > 0)) {
-          const float sub = m == -INFINITY ? 0.f : m;
+        // A tile inside the prefix: the exponents with the reference at hand, in one
+        // pass.  The general path takes over if a row has no reference yet (no key so
+        // far), a score lies outside the polynomial's range or above the reference's
+        // headroom.
+        if (!edge && (!TRACK || __all_sync(0xffffffffu, m != -INFINITY))) {
+          const float sub = m;
           const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
           const uint64_t step2 = f2_pack(2.f * slope2, 2.f * slope2);
-          uint64_t ls[2] = {l2[0], l2[1]};
+          uint32_t x[kKeys / 16][16];
+#pragma unroll
+          for (int c = 0; c < kKeys / 16; ++c) tmem_ld16(t_s + c * 16, x[c]);
+#pragma unroll
+          for (int c = 0; c < kKeys / 16; ++c) tmem_wait_ld16(x[c]);
+          // exponents of a pair of keys
+          auto exponents = [&](int c, int e, float base, uint64_t& add, float& a0, float& a1) {
+            const uint64_t v = f2_pack(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]));
+            uint64_t gf = sc2;
+            if (CAP) {
+              const uint64_t t = f2_mul(v, v);
+              gf = f2_pack(p.c[4], p.c[4]);
+#pragma unroll
+              for (int d = 3; d >= 0; --d) gf = f2_fma(gf, t, f2_pack(p.c[d], p.c[d]));
+            }
+            if (BIAS)
+              add = (e & 3) == 0 ? f2_pack(fmaf(slope2, (float)(2 * e), base), fmaf(slope2, (float)(2 * e + 1), base))
+                                 : f2_add(add, step2);
+            f2_unpack(f2_fma(v, gf, add), a0, a1);
+          };
+          // Does a score lie outside?  The largest product says so (its magnitude, for
+          // the polynomial), except with a bias, where the exponents are formed first.
           float am[2] = {0.f, 0.f}, sm[2] = {-INFINITY, -INFINITY};
-          uint32_t raw[2][32], pk[2][32];
-          tmem_ld32(t_s, raw[0]);
+          if (CAP || !BIAS) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&x)[32] = raw[c & 1];
-            tmem_wait_ld32(x);
-            if (c < 3) tmem_ld32(t_s + (c + 1) * 32, raw[(c + 1) & 1]);
-            const float base = BIAS ? -slope2 * (float)(pos - key0 - 32 * c) - sub : -sub;
-            uint64_t add = f2_pack(base, base);
+            for (int c = 0; c < kKeys / 16; ++c)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x0 = __uint_as_float(x[2 * e]), x1 = __uint_as_float(x[2 * e + 1]);
-              const uint64_t v = f2_pack(x0, x1);
-              uint64_t gf = sc2;
-              if (CAP) {
-                const uint64_t t = f2_mul(v, v);
-                gf = f2_pack(p.c[4], p.c[4]);
-#pragma unroll
-                for (int d = 3; d >= 0; --d) gf = f2_fma(gf, t, f2_pack(p.c[d], p.c[d]));
-                am[e & 1] = fmax3(am[e & 1], fabsf(x0), fabsf(x1));
+              for (int e = 0; e < 8; ++e) {
+                const float x0 = __uint_as_float(x[c][2 * e]), x1 = __uint_as_float(x[c][2 * e + 1]);
+                if (CAP) am[e & 1] = fmax3(am[e & 1], fabsf(x0), fabsf(x1));
+                else sm[e & 1] = fmax3(sm[e & 1], x0, x1);
               }
-              if (BIAS)
-                add = (e & 3) == 0 ? f2_pack(fmaf(slope2, (float)(2 * e), base), fmaf(slope2, (float)(2 * e + 1), base))
-                                   : f2_add(add, step2);
-              float a0, a1;
-              f2_unpack(f2_fma(v, gf, add), a0, a1);
-              if (TRACK) sm[e & 1] = fmax3(sm[e & 1], a0, a1);
-              const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
-              ls[e & 1] = f2_add(ls[e & 1], f2_pack(p0, p1));
-              pk[c >> 1][(c & 1) * 16 + e] = pack_bf16x2(p0, p1);  // the tensor core takes the weights in bf16
+          }
+          if (BIAS) {
+#pragma unroll
+            for (int c = 0; c < kKeys / 16; ++c) {
+              const float base = -slope2 * (float)(pos - key0 - 16 * c) - sub;
+              uint64_t add = 0;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float a0, a1;
+                exponents(c, e, base, add, a0, a1);
+                sm[e & 1] = fmax3(sm[e & 1], a0, a1);
+                x[c][2 * e] = __float_as_uint(a0);
+                x[c][2 * e + 1] = __float_as_uint(a1);
+              }
             }
           }
-          const bool redo = (CAP && fmaxf(am[0], am[1]) > p.x_lim) || (TRACK && fmaxf(sm[0], sm[1]) > kGrow);
+          const float amx = fmaxf(am[0], am[1]), smx = fmaxf(sm[0], sm[1]);
+          const bool redo = (CAP && amx > p.x_lim) || (BIAS && smx > kGrow) ||
+                            (MODE == kPlain && smx * p.scale_log2 - sub > kGrow) ||
+                            (MODE == kCapHigh && cap_score(amx, p) - sub > kGrow);
           if (!__any_sync(0xffffffffu, redo)) {
-            tmem_st32(t_s, pk[0]);
-            tmem_st32(t_s + 32, pk[1]);
-            l2[0] = ls[0];
-            l2[1] = ls[1];
+            free_s();
+            s_kept = false;
             done = true;
+            uint32_t pk[kKeys / 16][8];
+            uint64_t sub2 = f2_pack(-sub, -sub);
+#pragma unroll
+            for (int c = 0; c < kKeys / 16; ++c)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float a0 = __uint_as_float(x[c][2 * e]), a1 = __uint_as_float(x[c][2 * e + 1]);
+                if (!BIAS) exponents(c, e, 0.f, sub2, a0, a1);
+                const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+                l2[e & 1] = f2_add(l2[e & 1], f2_pack(p0, p1));
+                pk[c][e] = pack_bf16x2(p0, p1);  // the tensor core takes the weights in bf16
+              }
+            if (!wait_pv()) {
+              to = true;
+              break;
+            }
+#pragma unroll
+            for (int c = 0; c < kKeys / 16; ++c) tmem_st8(t_p + c * 8, pk[c]);
           }
         }
         if (!done) {
-          // the keys kc .. kc+31 that the row may read
+          // the keys kc .. kc+15 that the row may read
           auto allowed = [&](int kc) -> uint32_t {
             const int np = g.kl - kc;
             uint32_t w = np >= 32 ? ~0u : (np <= 0 ? 0u : (1u << np) - 1u);
             if (lo > kc) w &= lo - kc >= 32 ? 0u : ~0u << (lo - kc);
             const int r0 = kc - g.kl;  // tree row of bit 0
             if (r0 > -32 && r0 <= p.M) {
-              const uint32_t* a = p.anc + node * p.W;
+              const uint32_t* a = sh->anc[stid];
               uint32_t t;
               if (r0 <= 0) {
-                t = __ldg(a) << -r0;
+                t = a[0] << -r0;
               } else {
                 const int wi = r0 >> 5, sft = r0 & 31;
-                t = __ldg(a + wi) >> sft;
-                if (sft && wi + 1 < p.W) t |= __ldg(a + wi + 1) << (32 - sft);
+                t = a[wi] >> sft;
+                if (sft && wi + 1 < p.W) t |= a[wi + 1] << (32 - sft);
               }
               if (p.M + 1 - r0 < 32) t &= (1u << (p.M + 1 - r0)) - 1u;
               if (p.window > 0)
@@ -623,27 +694,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return w;
           };
+          if (!wait_pv()) {
+            to = true;
+            break;
+          }
           if (TRACK) {
             float mx = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t raw[32];
-              tmem_ld32(t_s + c * 32, raw);
-              const uint32_t ok = edge ? allowed(key0 + 32 * c) : ~0u;
-              tmem_wait_ld32(raw);
-              float x[32];
+            for (int c = 0; c < kKeys / 16; ++c) {
+              uint32_t raw[16];
+              tmem_ld16(t_s + c * 16, raw);
+              const uint32_t ok = edge ? allowed(key0 + 16 * c) : ~0u;
+              tmem_wait_ld16(raw);
+              float x[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(raw[e]);
-              chunk_scores<MODE>(x, p, edge, ok, 0.f, slope2, pos, key0 + 32 * c, g.kl, du, sh->depth);
+              for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(raw[e]);
+              chunk_scores<MODE>(x, p, edge, ok, 0.f, slope2, pos, key0 + 16 * c, g.kl, du, sh->depth);
               float a[2] = {fmaxf(mx, x[0]), x[1]};
 #pragma unroll
-              for (int e = 2; e < 32; e += 2) a[(e >> 1) & 1] = fmax3(a[(e >> 1) & 1], x[e], x[e + 1]);
+              for (int e = 2; e < 16; e += 2) a[(e >> 1) & 1] = fmax3(a[(e >> 1) & 1], x[e], x[e + 1]);
               mx = fmaxf(a[0], a[1]);
             }
             // The reference follows the maximum lazily: O is rescaled (a TMEM access of
             // the whole warp, each row by its own factor) only when some row's maximum
-            // has grown by more than 2^kGrow; then every row's follows.  A full S says
-            // that O is not in use.
+            // has grown by more than 2^kGrow; then every row's follows.
             const bool grow = __any_sync(0xffffffffu, mx > m + kGrow) ? mx > m : false;
             const bool scale_o = grow && m != -INFINITY;
             if (__any_sync(0xffffffffu, scale_o)) {
@@ -667,31 +741,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float sub = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t raw[32];
-            tmem_ld32(t_s + c * 32, raw);
-            const uint32_t ok = edge ? allowed(key0 + 32 * c) : ~0u;
-            tmem_wait_ld32(raw);
-            float x[32];
+          for (int c = 0; c < kKeys / 16; ++c) {
+            uint32_t raw[16];
+            tmem_ld16(t_s + c * 16, raw);
+            const uint32_t ok = edge ? allowed(key0 + 16 * c) : ~0u;
+            tmem_wait_ld16(raw);
+            float x[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(raw[e]);
-            chunk_scores<MODE>(x, p, edge, ok, sub, slope2, pos, key0 + 32 * c, g.kl, du, sh->depth);
-            uint32_t pk[16];
+            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(raw[e]);
+            chunk_scores<MODE>(x, p, edge, ok, sub, slope2, pos, key0 + 16 * c, g.kl, du, sh->depth);
+            uint32_t pk[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 8; ++e) {
               const float p0 = fast_exp2(x[2 * e]), p1 = fast_exp2(x[2 * e + 1]);
               l2[e & 1] = f2_add(l2[e & 1], f2_pack(p0, p1));
               pk[e] = pack_bf16x2(p0, p1);
             }
-            tmem_st16(t_s + c * 16, pk);
+            tmem_st8(t_p + c * 8, pk);
           }
         }
         tmem_wait_st();
+      } else if (!wait_pv()) {  // (no row of this warp is real; a parity wait must not fall behind)
+        to = true;
+        break;
       }
-      // V rows behind the step's may hold anything: zero them (the first pipe's
-      // warps for both pipes where they share the tile; its PV is issued first)
-      const int kend = g.kl + p.M + 1 - (g.first + (nt - 1 - j) * kKeys);
-      if (kend < kKeys && (!dual || pipe == 0)) {
+      if (s_kept) free_s();
+      // V rows behind the step's may hold anything: zero them (where the pipes share
+      // the tile, both do, each before its own product)
+      const int kend = g.kl + p.M + 1 - key0;
+      if (kend < kKeys) {
         const uint32_t idx = base + v_idx(g, j), s = idx % kSlots;
         if (!__all_sync(0xffffffffu, mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim))) {
           to = true;
@@ -714,10 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       f2_unpack(l2[1], s2, s3);
       l += (s0 + s1) + (s2 + s3);
     }
-    if (n > 0 && !to && !mbar_wait(&sh->o_full[pipe], done_o[pipe] & 1, lim)) to = true;
-    // (the second pipe's hand-over below goes through the query tile, which the
-    // first one's products must have read)
-    if (!dual && nt > 0 && pipe == 1 && !to && !mbar_wait(&sh->o_full[0], done_o[0] & 1, lim)) to = true;
+    if (n > 0 && !to && !mbar_wait(&sh->pv_done[pipe], (step0 + n - 1) & 1, lim)) to = true;
     to = __any_sync(0xffffffffu, to);
     const bool have = n > 0 && !to;
     if (to && lane == 0) {
@@ -735,6 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float4* join_o = reinterpret_cast<float4*>(q_s);  // [D / 4][128]
     float w0 = 1.f, w1 = 0.f;
     if (!dual) {
+      asm volatile("bar.sync 3, 256;" ::: "memory");  // both pipes' products have read the query tile
       if (pipe == 1) {
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -769,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
       w0 *= inv;
       w1 *= inv;
-      uint8_t* stage = q_s + pipe * kTile;  // of a pair: this pipe's query tile, [128 rows][2 D bytes], chunks rotated
+      uint8_t* stage = q_s + pipe * kQTile;  // of a pair: this pipe's query tile, [128 rows][2 D bytes], chunks rotated
       const int64_t rec = 2 * (int64_t)g.index + pipe;
       float4* dst = reinterpret_cast<float4*>(p.ws_o) + rec * (D / 4) * p.rec_rows;
       uint4* out_row = reinterpret_cast<uint4*>(p.out + query_row(p, b, hk, min(gr, p.rows - 1)) * D);
@@ -823,11 +899,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __stcg(p.ws_ml + rec * p.rec_rows + r, make_float2(m, l));
       }
     }
-    if (g.sl < 0 && tid == 128) atomicOr(&p.status[b], kSeqBadGeometry);
+    if (g.sl < 0 && stid == 0) atomicOr(&p.status[b], kSeqBadGeometry);
     base += 2 * nt;
     step0 += n;
-    if (nt > 0) ++done_o[0];
-    if (dual ? nt > 0 : nt > 1) ++done_o[1];
     // the query tiles and depths are free for the next item
     asm volatile("bar.sync 3, 256;" ::: "memory");
     if (lane == 0) mbar_arrive(&sh->item_empty[n_item & 1]);
@@ -907,7 +981,7 @@ __global__ void __launch_bounds__(256) scored_merge_kernel(const __grid_constant
   }
   }
 
-// [BH][S_cap][D] bf16 in boxes of 128 rows: 64 columns (D = 64), or both 64-column
+// [BH][S_cap][D] bf16 in boxes of kKeys rows: 64 columns (D = 64), or both 64-column
 // halves of a row (D = 128), landing as [half][row][128 B], 128-byte swizzle.
 bool encode_scored_map(CUtensorMap* map, const void* base, int64_t BH, int64_t S_cap, int D) {
   EncodeTiledFn enc = get_encode_fn();
@@ -969,7 +1043,7 @@ tv_status launch_scored(int mode, const CUtensorMap& tmk, const CUtensorMap& tmv
               : mode == kCapHigh ? scored_kernel<D, kCapHigh>
               : mode == kBias    ? scored_kernel<D, kBias>
                                  : scored_kernel<D, kCapBias>;
-  const size_t smem = 2 * (D / 64) * kHalf + kRingBytes + sizeof(Shared);
+  const size_t smem = 2 * (D / 64) * kQHalf + kRingBytes + sizeof(Shared);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return record_cuda_error(e);
   tv_status r = launch(kern, dim3((unsigned)lp.grid), dim3(kThreads), smem, s, 1, true, tmk, tmv, p);
