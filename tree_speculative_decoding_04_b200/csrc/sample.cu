@@ -11,25 +11,59 @@
 // drawn token is the first kept one, in vocabulary order, whose inclusive
 // weight exceeds u times the kept weight.
 //
-// A prefix is named by its last key t (a float's order-preserving bits) and the
-// number c of tokens equal to t that belong to it.  Weights are formed in double
-// precision and summed as 64-bit fixed-point integers: the sums do not depend
-// on the order or the split of the work, and their error is far below the
-// weight of any token that can be drawn.
+// Launches, each over the whole GPU:
+//   stream  one pass over the logits (a chunk of 1024 per warp, loads of 128 bytes
+//           that need no alignment): the maximum of every 128 tokens and, for rows
+//           without a filter, each chunk's weight relative to its maximum
+//   finish  a block per row.  No filter: the chunk in which the target falls is
+//           read again.  Top-k, min-p: no token below a bound can be kept or matter
+//           (top-k: the k-th largest of the 128-token maxima bounds the k-th largest
+//           token; min-p: its threshold), so only 128-token blocks that reach it are
+//           read again; the tokens that do go to a list in shared memory, in
+//           vocabulary order (were it to overflow, they are walked in L2 instead),
+//           and a radix selection over histograms of (count, weight) finds the kept
+//           prefix.  Top-p over the whole vocabulary can keep tens of thousands of
+//           tokens; its rows go through two more launches:
+//   weigh   a histogram of weights over 1/32-octave bins below the row's maximum; the
+//           block that brings a row's last segment finds the bin of the border
+//   border  the weight that each chunk keeps for sure, and a list of the tokens in
+//           the border's bin; the last block of a row settles that bin and draws
+//   walk    tree_accept's acceptance walk, on the drawn tokens
+// Weights are doubles (2^((l - m) log2e / T), relative error below 2^-48: a
+// token's share of a flat vocabulary is 2^-18, and a sum in fp32 would move the
+// borders between tokens by as much).  Histograms hold them as 64-bit fixed-point
+// numbers, and all other sums run in a fixed order, so results do not depend on
+// the order of the work.
+//
+// Bound by HBM for large batches (the logits are read once, rows with top-p three
+// times), by launches and block-wide steps for a few rows.
 #include <algorithm>
+#include <climits>
 
 #include "tv_common.cuh"
 
 namespace tv {
 namespace {
 
-constexpr int kSampleThreads = 512;
-constexpr int kMaxVocab = 1 << 18;  // fixed-point weights of one row stay below 2^63
+typedef unsigned long long u64;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = 1024;             // tokens per warp and pass
+constexpr int kSub = 128;                // tokens per recorded maximum
+constexpr int kMaxVocab = 1 << 18;       // fixed-point weights of one row stay below 2^63
+constexpr int kMaxSubs = kMaxVocab / kSub;
+static_assert(kMaxVocab / kChunk <= kThreads, "one thread per chunk in the finish");
+constexpr int kListCap = 512;            // listed tokens per warp
+constexpr int kBins = 1024;
+constexpr int kTab = 128;
+
+struct RowState;
 
 struct SampleParams {
   const void* logits;
-  int64_t stride;
-  int V, n;
+  int64_t stride, rows;
+  int V, n, nseg, nsub, nchunk;
   const float* uniform;
   const float* temperature;
   const int32_t* top_k;
@@ -37,7 +71,38 @@ struct SampleParams {
   const float* min_p;
   int32_t* token;
   float* logprob;
-  int shift;  // weight 1 is 2^shift
+  float* sub;    // [rows][nsub] maxima of 128 tokens
+  double* sum;   // [rows][nchunk] weight of a chunk: all, relative to its maximum, or kept for sure
+  // rows with top-p over the whole vocabulary
+  int* marked;         // [0] how many, [1 + i] their rows
+  RowState* st;        // [rows]
+  u64* hist;           // [rows][kBins] weights
+  float* list_x;       // [rows][kRowList] tokens in the border's bin
+  int* list_i;
+  int shift;     // weight 1 is 2^shift in the histograms
+};
+
+constexpr int kRowList = kWarps * kListCap;
+
+struct RowState {
+  u64 above, total;       // weight above the border's bin, of all tokens (fixed point)
+  float m, scale;         // maximum; bins per unit of logit
+  int bin, listed;        // the border's bin; tokens in it
+  int weighed, bordered;  // segments that have arrived
+};
+
+struct Shared {
+  double tab[kTab];  // 2^(i / kTab)
+  double cs;
+  double redd[kWarps];
+  u64 red[kWarps];
+  float sub[kMaxSubs];
+  uint32_t cnt[kBins], lo[kBins], hi[kBins];
+  float lval[kWarps][kListCap];
+  int lidx[kWarps][kListCap];
+  int len[kWarps];
+  int found, found2, last, last2;
+  u64 found_mass;
 };
 
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -48,220 +113,903 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-template <typename T>
-__device__ __forceinline__ T block_sum(T v, T* red) {
+// 2^y for y <= 0: y = n / 128 + r, |r| <= 1/256; 2^r by the first five terms of
+// its series (the next is below 2^-49 of the result), 2^(n / 128) from the table
+// and the exponent field.  0 below 2^-1000 and for NaN.
+__device__ __forceinline__ double pow2(double y, const double* tab) {
+  if (!(y > -1000.0)) return 0.0;
+  const double magic = 6755399441055744.0;  // 1.5 * 2^52: rounds to an integer
+  const double t = fma(y, (double)kTab, magic);
+  const int n = __double2loint(t);
+  const double r = fma(t - magic, -1.0 / kTab, y);
+  double q = 0.0096181291076284772;  // ln2^4 / 24
+  q = fma(q, r, 0.055504108664821580);
+  q = fma(q, r, 0.24022650695910071);
+  q = fma(q, r, 0.69314718055994531);
+  const double v = tab[n & (kTab - 1)] * fma(q, r, 1.0);
+  return __hiloint2double(__double2hiint(v) + ((n >> 7) << 20), __double2loint(v));
+}
+
+// Weight of logit x relative to the maximum m, c = log2(e) / T.
+__device__ __forceinline__ double weight(float x, float m, double c, const double* tab) {
+  if (x == m) return x == -INFINITY ? 0.0 : 1.0;
+  if (x == -INFINITY || m == INFINITY) return 0.0;
+  return pow2(((double)x - (double)m) * c, tab);
+}
+
+// NaN counts as -inf (never drawn); -0 as +0
+__device__ __forceinline__ float clean(float x) { return x == x ? x + 0.f : -INFINITY; }
+
+template <bool BF16>
+__device__ __forceinline__ float logit(const SampleParams& p, int64_t row, int i) {
+  if (BF16) return clean(__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.logits)[row * p.stride + i]));
+  return clean(reinterpret_cast<const float*>(p.logits)[row * p.stride + i]);
+}
+
+__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+__device__ __forceinline__ double warp_scan(double v) {  // inclusive
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const double o = __shfl_up_sync(0xffffffffu, v, off);
+    if ((int)(threadIdx.x & 31) >= off) v += o;
+  }
+  return v;
+}
+__device__ __forceinline__ u64 warp_scan(u64 v) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const u64 o = __shfl_up_sync(0xffffffffu, v, off);
+    if ((int)(threadIdx.x & 31) >= off) v += o;
+  }
+  return v;
+}
+
+// 1/32-octave bin of a token below the row's maximum (monotone in x; infinities
+// and NaN of the difference go to the ends).
+__device__ __forceinline__ int bin_of(float x, const RowState& r) {
+  if (x == r.m) return 0;
+  const float d = (r.m - x) * r.scale;
+  return d < (float)(kBins - 1) ? (int)d : kBins - 1;
+}
+
+// Settings of a row's sequence.
+struct Rule {
+  float T, top_p, min_p;
+  int k;  // 0: off
+  bool greedy, use_p, use_m, plain;  // plain: no filter
+  double c;  // log2(e) / T
+};
+__device__ __forceinline__ Rule rule_of(const SampleParams& p, int b) {
+  Rule r;
+  r.T = p.temperature[b];
+  r.greedy = !(r.T > 0.f);
+  r.c = r.greedy ? 1.0 : 1.4426950408889634 / (double)r.T;
+  const int k = p.top_k ? p.top_k[b] : 0;
+  r.k = k > 0 && k < p.V ? k : 0;
+  r.top_p = p.top_p ? p.top_p[b] : 1.f;
+  r.min_p = p.min_p ? p.min_p[b] : 0.f;
+  r.use_p = r.top_p < 1.f;  // false for NaN
+  r.use_m = r.min_p > 0.f;
+  r.plain = !r.greedy && r.k == 0 && !r.use_p && !r.use_m;
+  return r;
+}
+
+// The tokens that may matter to a row with filters: the list, or (overflown) the
+// 128-token blocks that reach the bound.  Warp w owns a contiguous range of the
+// vocabulary; walk() visits it in order, 32 tokens at a time.
+template <bool BF16>
+struct Source {
+  const SampleParams& p;
+  Shared& sh;
+  int64_t row;
+  float bound;
+  bool listed;
+
+  template <class F>
+  __device__ __forceinline__ void blocks(F f) const {  // f(first token, x[4]) for each of the warp's blocks
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b0 = (int)((int64_t)p.nsub * w / kWarps), b1 = (int)((int64_t)p.nsub * (w + 1) / kWarps);
+    for (int base = b0; base < b1; base += 32) {
+      unsigned m = __ballot_sync(0xffffffffu, base + lane < b1 && sh.sub[min(base + lane, b1 - 1)] >= bound);
+      while (m) {
+        int blk[4];
+        float x[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // four blocks' loads in flight
+          blk[k] = m ? base + __ffs(m) - 1 : -1;
+          m &= m - 1;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int i = blk[k] * kSub + j * 32 + lane;
+            x[k][j] = blk[k] >= 0 && i < p.V ? logit<BF16>(p, row, i) : -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (blk[k] >= 0) f(blk[k] * kSub, x[k]);
+      }
+    }
+  }
+  template <class F>
+  __device__ __forceinline__ void walk(F f) const {  // f(x, index, present), warp-collective
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (listed) {
+      for (int i0 = 0; i0 < sh.len[w]; i0 += 32) {
+        const bool in = i0 + lane < sh.len[w];
+        f(in ? sh.lval[w][i0 + lane] : -INFINITY, in ? sh.lidx[w][i0 + lane] : 0, in);
+      }
+    } else {
+      blocks([&](int first, const float(&x)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f(x[j], first + j * 32 + lane, x[j] >= bound && x[j] > -INFINITY);
+      });
+    }
+  }
+};
+
+// A border of the order: keys above t, and the first c of the `ties` tokens with key t.
+struct Border {
+  uint32_t t;
+  int c, ties;
+};
+
+// The key in [lo, hi] at which the tokens from the top first count `want` (MASS =
+// false) or first weigh `want` (MASS), by histograms over ever narrower key
+// ranges.  key(x, index): keys outside the range are left out.  above: the count
+// or weight above `hi` on entry, above the found key on return; ties: tokens with
+// that key.  False if all tokens together do not reach it.
+template <bool MASS, class Src, class Key>
+__device__ bool select(const Src& src, Shared& sh, Key key, uint32_t lo, uint32_t hi, double want, float m, double c,
+                       int shift, uint32_t& t, u64& above, int& ties) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  for (;;) {
+    const uint32_t range = hi - lo;
+    const int sh_bits = max(0, 32 - __clz(range) - 10);
+    __syncthreads();
+    for (int i = tid; i < kBins; i += kThreads) {
+      sh.cnt[i] = 0;
+      if (MASS) sh.lo[i] = sh.hi[i] = 0;
+    }
+    if (tid == 0) sh.found = -1;
+    __syncthreads();
+    src.walk([&](float x, int i, bool in) {
+      const uint32_t k = in ? key(x, i) : 0u;
+      if (!in || k < lo || k > hi) return;
+      const int bin = (int)((k - lo) >> sh_bits);
+      atomicAdd(&sh.cnt[bin], 1u);
+      if (MASS) {
+        const u64 wt = (u64)__double2ull_rn(weight(x, m, c, sh.tab) * (double)(1ull << shift));
+        const uint32_t l = (uint32_t)wt, old = atomicAdd(&sh.lo[bin], l);
+        const uint32_t h = (uint32_t)(wt >> 32) + (old + l < old ? 1u : 0u);
+        if (h) atomicAdd(&sh.hi[bin], h);
+      }
+    });
+    __syncthreads();
+    // from the top: thread i sums bins 1023 - 4 i .. 1020 - 4 i
+    u64 v[4], s = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int bin = kBins - 1 - 4 * tid - j;
+      v[j] = MASS ? ((u64)sh.hi[bin] << 32) + sh.lo[bin] : sh.cnt[bin];
+      s += v[j];
+    }
+    u64 incl = warp_scan(s);
+    if (lane == 31) sh.red[w] = incl;
+    __syncthreads();
+    for (int i = 0; i < w; ++i) incl += sh.red[i];
+    u64 cum = above + incl - s;
+    if ((double)cum < want && (double)(cum + s) >= want) {  // one thread at most
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if ((double)(cum + v[j]) >= want) {
+          sh.found = kBins - 1 - 4 * tid - j;
+          sh.found_mass = cum;
+          break;
+        }
+        cum += v[j];
+      }
+    }
+    __syncthreads();
+    const int bin = sh.found;
+    if (bin < 0) return false;
+    above = sh.found_mass;
+    ties = (int)sh.cnt[bin];
+    lo += (uint32_t)bin << sh_bits;
+    if (sh_bits == 0) break;
+    hi = min(hi, lo + ((1u << sh_bits) - 1u));
+  }
+  t = lo;
+  return true;
+}
+
+// How many of `ties` tokens of weight wt, behind a weight of `above`, have less than
+// `want` before them (at least one).
+__device__ __forceinline__ int tokens_below(u64 above, u64 wt, int ties, double want) {
+  u64 l = 0, h = (u64)ties;
+  while (l < h) {
+    const u64 mid = (l + h) / 2;
+    if ((double)(above + mid * wt) < want) l = mid + 1;
+    else h = mid;
+  }
+  return max(1, (int)l);
+}
+
+// Inclusive scan of one double per thread, and the total, in a fixed order.
+__device__ __forceinline__ double block_scan(double v, Shared& sh, double& total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  double incl = warp_scan(v);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if (lane == 31) sh.redd[w] = incl;
   __syncthreads();
-  T s = 0;
-  for (int i = 0; i < kSampleThreads / 32; ++i) s += red[i];
+  double before = 0.0, all = 0.0;
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < w) before += sh.redd[i];
+    all += sh.redd[i];
+  }
+  total = all;
+  return before + incl;
+}
+
+// The last of the c first (in vocabulary order) among the tokens with key t.
+template <class Src, class Key>
+__device__ int tie_limit(const Src& src, Shared& sh, Key key, uint32_t t, int c) {
+  uint32_t end = 0;
+  u64 above = 0;
+  int one;
+  select<false>(
+      src, sh, [&](float x, int i) { return key(x, i) == t ? (uint32_t)(kMaxVocab - i) : 0u; }, 1u, kMaxVocab, (double)c,
+      0.f, 0.0, 0, end, above, one);
+  return kMaxVocab - (int)end;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void put(const SampleParams& p, int64_t row, int tok, double lp) {
+  p.token[row] = tok;
+  if (p.logprob) p.logprob[row] = (float)lp;
+}
+
+// Draws from a row whose chunks weigh `own` (thread i: chunk i).  kept(x, index):
+// the token counts.
+template <bool BF16, class Kept>
+__device__ void draw(const SampleParams& p, Shared& sh, int64_t row, double own, float m, double c, Kept kept) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  double total;
+  const double incl = block_scan(own, sh, total);
+  const double target = (double)p.uniform[row] * total;
+  if (tid == 0) {
+    sh.found = sh.found2 = INT_MAX;
+    sh.last = sh.last2 = -1;
+  }
+  __syncthreads();
+  if (own > 0.0) {
+    if (incl > target) atomicMin(&sh.found, tid);
+    atomicMax(&sh.last, tid);
+  }
+  __syncthreads();
+  const int chunk = sh.found != INT_MAX ? sh.found : sh.last;
+  if (tid == chunk) sh.cs = incl - own;
+  // a warp takes 128 tokens of the chunk
+  float x[4];
+  double v[4], s = 0.0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = chunk * kChunk + w * 128 + j * 32 + lane;
+    x[j] = i < p.V ? logit<BF16>(p, row, i) : -INFINITY;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = chunk * kChunk + w * 128 + j * 32 + lane;
+    v[j] = warp_scan(kept(x[j], i) ? weight(x[j], m, c, sh.tab) : 0.0);
+    s += __shfl_sync(0xffffffffu, v[j], 31);
+  }
+  if (lane == 0) sh.redd[w] = s;
+  __syncthreads();
+  double cum = sh.cs;
+  for (int i = 0; i < w; ++i) cum += sh.redd[i];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = chunk * kChunk + w * 128 + j * 32 + lane;
+    const bool has = kept(x[j], i) && weight(x[j], m, c, sh.tab) > 0.0;
+    if (has && cum + v[j] > target) atomicMin(&sh.found2, i);
+    if (has) atomicMax(&sh.last2, i);
+    cum += __shfl_sync(0xffffffffu, v[j], 31);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    // (a target at the very end of the chunk: its last kept token)
+    const int tok = sh.found2 != INT_MAX ? sh.found2 : sh.last2;
+    const float xt = logit<BF16>(p, row, tok);
+    put<BF16>(p, row, tok, (xt == m ? 0.0 : ((double)xt - (double)m) * c * 0.69314718055994531) - log(total));
+  }
+}
+
+// A row with filters, from the tokens that reach `bound`; base: the weight of all
+// tokens (fixed point), for top-p without top-k.
+template <bool BF16>
+__device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const Rule& r, float m, float bound, float cut,
+                         u64 base) {
+  constexpr int kDrop = BF16 ? 16 : 0;  // a bf16's key has 16 bits
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const double c = r.c;
+  const uint32_t mkey = order_key(m);
+  auto key = [](float x, int) { return order_key(x) >> kDrop; };
+  Source<BF16> src{p, sh, row, bound, false};
+  int len = 0;
+  src.blocks([&](int first, const float(&x)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool in = x[j] >= bound && x[j] > -INFINITY;
+      const unsigned b = __ballot_sync(0xffffffffu, in);
+      const int at = len + __popc(b & ((1u << lane) - 1u));
+      if (in && at < kListCap) {
+        sh.lval[w][at] = x[j];
+        sh.lidx[w][at] = first + j * 32 + lane;
+      }
+      len += __popc(b);
+    }
+  });
+  if (lane == 0) sh.len[w] = len;
+  src.listed = __syncthreads_and(len <= kListCap) != 0;
+  int present = 0;
+  for (int i = 0; i < kWarps; ++i) present += sh.len[i];
+
+  // ---------------------------------------------------------------- the kept prefix
+  const uint32_t klo = order_key(bound) >> kDrop, khi = mkey >> kDrop;
+  Border e{klo, INT_MAX, 0};  // everything present
+  if (r.k > 0 && present > r.k) {
+    u64 above = 0;
+    select<false>(src, sh, key, klo, khi, (double)r.k, m, c, p.shift, e.t, above, e.ties);
+    e.c = r.k - (int)above;
+  }
+  auto value = [&](uint32_t t) { return BF16 ? key_value(t << 16 | ((t & 0x8000u) ? 0u : 0xffffu)) : key_value(t); };
+  auto fixed = [&](float x) { return (u64)__double2ull_rn(weight(x, m, c, sh.tab) * (double)(1ull << p.shift)); };
+  if (r.use_p) {
+    if (r.k > 0) {  // the weight of the top k
+      u64 s = 0;
+      src.walk([&](float x, int, bool in) {
+        if (in && order_key(x) >> kDrop >= e.t) s += fixed(x);
+      });
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      __syncthreads();
+      if (lane == 0) sh.red[w] = s;
+      __syncthreads();
+      base = 0;
+      for (int i = 0; i < kWarps; ++i) base += sh.red[i];
+      if (e.c < e.ties) base -= (u64)(e.ties - e.c) * fixed(value(e.t));
+    }
+    const double want = (double)r.top_p * (double)base;
+    uint32_t t;
+    int ties;
+    u64 above = 0;
+    if (select<true>(src, sh, key, e.t, khi, want, m, c, p.shift, t, above, ties)) {
+      // tokens of key t that are kept: while the weight before them is below `want`
+      const int q = tokens_below(above, fixed(value(t)), t == e.t ? min(e.c, ties) : ties, want);
+      e = Border{t, q, ties};
+    }
+  }
+  const int tie_end = e.c < e.ties ? tie_limit(src, sh, key, e.t, e.c) : INT_MAX;
+
+  // ---------------------------------------------------------------- the draw
+  auto kept = [&](float x, int i, bool in) -> double {
+    const uint32_t k = order_key(x) >> kDrop;
+    if (!in || k < e.t || (k == e.t && i > tie_end) || !(x >= cut || x == m)) return 0.0;
+    return weight(x, m, c, sh.tab);
+  };
+  double s = 0.0;
+  src.walk([&](float x, int i, bool in) { s += kept(x, i, in); });
+  s = warp_sum(s);
+  __syncthreads();
+  if (lane == 0) sh.redd[w] = s;
+  __syncthreads();
+  double total = 0.0;
+  for (int i = 0; i < kWarps; ++i) total += sh.redd[i];
+  const double target = (double)p.uniform[row] * total;
+  int owner = -1, last_w = 0;
+  double cum = 0.0, before = 0.0;
+  for (int i = 0; i < kWarps; ++i) {
+    if (sh.redd[i] > 0.0) last_w = i;
+    if (owner < 0 && cum + sh.redd[i] > target) {
+      owner = i;
+      before = cum;
+    }
+    cum += sh.redd[i];
+  }
+  const bool at_end = owner < 0;  // a target at the very end: the last kept token
+  if (at_end) owner = last_w;
+  if (w == owner) {
+    int tok = -1, last = -1;
+    float tx = m, lx = m;
+    src.walk([&](float x, int i, bool in) {
+      if (tok >= 0) return;
+      const double v = kept(x, i, in);
+      const double sc = warp_scan(v);
+      const unsigned has = __ballot_sync(0xffffffffu, v > 0.0);
+      const unsigned hit = __ballot_sync(0xffffffffu, v > 0.0 && !at_end && before + sc > target);
+      if (has) {
+        last = __shfl_sync(0xffffffffu, i, 31 - __clz(has));
+        lx = __shfl_sync(0xffffffffu, x, 31 - __clz(has));
+      }
+      if (hit) {
+        tok = __shfl_sync(0xffffffffu, i, __ffs(hit) - 1);
+        tx = __shfl_sync(0xffffffffu, x, __ffs(hit) - 1);
+      }
+      before += __shfl_sync(0xffffffffu, sc, 31);
+    });
+    if (tok < 0) {
+      tok = last;
+      tx = lx;
+    }
+    if (lane == 0)
+      put<BF16>(p, row, tok, (tx == m ? 0.0 : ((double)tx - (double)m) * c * 0.69314718055994531) - log(total));
+  }
+}
+
+__device__ __forceinline__ float min_p_cut(const Rule& r, float m) {
+  return r.use_m ? fmaxf(-INFINITY, __double2float_ru((double)m + log2((double)r.min_p) / r.c)) : -INFINITY;
+}
+
+template <bool BF16>
+__device__ void finish_row(const SampleParams& p, Shared& sh, int64_t row) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const Rule r = rule_of(p, (int)(row / p.n));
+  float mx = -INFINITY;
+  for (int i = tid; i < p.nsub; i += kThreads) {
+    const float s = __ldcg(p.sub + row * p.nsub + i);
+    sh.sub[i] = s;
+    mx = fmaxf(mx, s);
+  }
+  const uint32_t wk = __reduce_max_sync(0xffffffffu, order_key(mx));
+  if (lane == 0) sh.red[w] = wk;
+  if (tid == 0) sh.found = sh.found2 = INT_MAX;
+  __syncthreads();
+  uint32_t mkey = 0;
+  for (int i = 0; i < kWarps; ++i) mkey = max(mkey, (uint32_t)sh.red[i]);
+  const float m = key_value(mkey);
+  if (m == -INFINITY) {  // no token can be drawn
+    if (tid == 0) put<BF16>(p, row, -1, -INFINITY);
+    return;
+  }
+  if (r.greedy || r.k == 1 || (r.use_p && !(r.top_p > 0.f)) || r.min_p > 1.f) {  // the first token of the order
+    for (int i = tid; i < p.nsub; i += kThreads)
+      if (sh.sub[i] == m) {
+        atomicMin(&sh.found, i);
+        break;
+      }
+    __syncthreads();
+    const int i = sh.found * kSub + tid;
+    if (tid < kSub && i < p.V && logit<BF16>(p, row, i) == m) atomicMin(&sh.found2, i);
+    __syncthreads();
+    if (tid == 0) put<BF16>(p, row, sh.found2, 0.0);
+    return;
+  }
+  if (r.k == 0 && r.use_p) {  // on to the weighing
+    u64* h = p.hist + row * kBins;
+    for (int i = tid; i < kBins; i += kThreads) __stcg(h + i, 0ull);
+    if (tid == 0) {
+      RowState st = {};
+      st.m = m;
+      st.scale = (float)fmin(32.0 * r.c, 3e38);
+      p.st[row] = st;
+      p.marked[1 + atomicAdd(p.marked, 1)] = (int)row;
+    }
+    return;
+  }
+  if (r.plain) {
+    double own = 0.0;
+    if (tid < p.nchunk) {
+      float cm = -INFINITY;
+      for (int i = tid * (kChunk / kSub); i < min(p.nsub, (tid + 1) * (kChunk / kSub)); ++i) cm = fmaxf(cm, sh.sub[i]);
+      own = __ldcg(p.sum + row * p.nchunk + tid) * weight(cm, m, r.c, sh.tab);
+    }
+    draw<BF16>(p, sh, row, own, m, r.c, [](float, int) { return true; });
+    return;
+  }
+  const float cut = min_p_cut(r, m);
+  float bound = -INFINITY;
+  if (r.k > 0 && r.k <= p.nsub) {
+    // a value that at least k of the 128-token maxima reach
+    uint32_t lowest = 0xffffffffu;
+    for (int i = tid; i < p.nsub; i += kThreads) lowest = min(lowest, order_key(sh.sub[i]));
+    lowest = __reduce_min_sync(0xffffffffu, lowest);
+    __syncthreads();
+    if (lane == 0) sh.red[w] = lowest;
+    for (int i = tid; i < kBins; i += kThreads) sh.cnt[i] = 0;
+    __syncthreads();
+    for (int i = 0; i < kWarps; ++i) lowest = min(lowest, (uint32_t)sh.red[i]);
+    const int bits = max(0, 32 - __clz(mkey - lowest) - 10);
+    for (int i = tid; i < p.nsub; i += kThreads) atomicAdd(&sh.cnt[(order_key(sh.sub[i]) - lowest) >> bits], 1u);
+    __syncthreads();
+    u64 s = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s += sh.cnt[kBins - 1 - 4 * tid - j];
+    u64 in = warp_scan(s);
+    __syncthreads();
+    if (lane == 31) sh.red[w] = in;
+    __syncthreads();
+    for (int i = 0; i < w; ++i) in += sh.red[i];
+    if (in >= (u64)r.k && in - s < (u64)r.k) {
+      u64 cum = in - s;
+      for (int j = 0; j < 4; ++j) {
+        cum += sh.cnt[kBins - 1 - 4 * tid - j];
+        if (cum >= (u64)r.k) {
+          sh.found = kBins - 1 - 4 * tid - j;
+          break;
+        }
+      }
+    }
+    __syncthreads();
+    bound = key_value(lowest + ((uint32_t)sh.found << bits));
+  }
+  if (!r.use_p) bound = fmaxf(bound, cut);  // (top-p's base holds all of the top k)
+  filtered<BF16>(p, sh, row, r, m, fminf(bound, m), cut, 0);
+}
+
+// A warp's chunk of 1024 logits, cleaned.  Lane's tokens: 32 j + lane (fp32), 64 j +
+// 2 lane and the next (bf16); token(e) is the index of x[e] in the chunk, and block
+// s of 128 tokens is x[4 s .. 4 s + 3].
+template <bool BF16>
+__device__ __forceinline__ int chunk_token(int e) {
+  const int lane = threadIdx.x & 31;
+  return BF16 ? (e >> 1) * 64 + 2 * lane + (e & 1) : e * 32 + lane;
+}
+template <bool BF16>
+__device__ __forceinline__ void load_chunk(const SampleParams& p, int64_t row, int chunk, uint32_t (&raw)[BF16 ? 16 : 32]) {
+  const int lane = threadIdx.x & 31, i0 = chunk * kChunk;
+  if (BF16) {
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(p.logits) + row * p.stride + i0;
+    if ((reinterpret_cast<uintptr_t>(src) & 3u) == 0 && i0 + kChunk <= p.V) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) raw[j] = __ldg(reinterpret_cast<const uint32_t*>(src) + j * 32 + lane);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int i = j * 64 + 2 * lane;
+        const uint32_t a = i0 + i < p.V ? __ldg(src + i) : 0xff80u, b = i0 + i + 1 < p.V ? __ldg(src + i + 1) : 0xff80u;
+        raw[j] = a | b << 16;
+      }
+    }
+  } else {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.logits) + row * p.stride + i0;
+    if (i0 + kChunk <= p.V) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) raw[j] = __ldg(src + j * 32 + lane);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) raw[j] = i0 + j * 32 + lane < p.V ? __ldg(src + j * 32 + lane) : 0xff800000u;
+    }
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void clean_chunk(const uint32_t (&raw)[BF16 ? 16 : 32], float (&x)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    x[e] = clean(__uint_as_float(!BF16 ? raw[BF16 ? 0 : e] : ((e & 1) ? raw[BF16 ? e >> 1 : 0] & 0xffff0000u : raw[BF16 ? e >> 1 : 0] << 16)));
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 4) stream_kernel(const __grid_constant__ SampleParams p) {
+  __shared__ double tab[kTab];
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < kTab) tab[tid] = exp2((double)tid / kTab);
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (blockIdx.x == 0 && tid == 0) p.marked[0] = 0;
+  __syncthreads();
+  const int64_t units = p.rows * p.nchunk, step = (int64_t)gridDim.x * kWarps;
+  int64_t unit = (int64_t)blockIdx.x * kWarps + (tid >> 5);
+  for (; unit < units; unit += step) {
+    const int64_t row = unit / p.nchunk;
+    const int chunk = (int)(unit - row * p.nchunk);
+    uint32_t raw[BF16 ? 16 : 32];
+    load_chunk<BF16>(p, row, chunk, raw);
+    const Rule r = rule_of(p, (int)(row / p.n));
+    float x[32];
+    clean_chunk<BF16>(raw, x);
+    uint32_t top = 0, mine = 0;
+#pragma unroll
+    for (int s = 0; s < kChunk / kSub; ++s) {
+      const uint32_t k = __reduce_max_sync(
+          0xffffffffu, order_key(fmaxf(fmaxf(x[4 * s], x[4 * s + 1]), fmaxf(x[4 * s + 2], x[4 * s + 3]))));
+      if (lane == s) mine = k;
+      top = max(top, k);
+    }
+    const int sub0 = chunk * (kChunk / kSub);
+    if (lane < kChunk / kSub && sub0 + lane < p.nsub) __stcg(p.sub + row * p.nsub + sub0 + lane, key_value(mine));
+    if (r.plain) {
+      const float cm = key_value(top);
+      double s = 0.0;
+      if (cm < INFINITY && cm > -INFINITY) {
+        // (far below the maximum 2^-900 stands for the weight)
+        const double off = -(double)cm * r.c;
+        const float far = (float)fmax((double)cm - 900.0 / r.c, -3e38);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const double v = pow2(fma((double)fmaxf(x[e], far), r.c, off), tab);
+          s += x[e] > -INFINITY ? v : 0.0;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s += weight(x[e], cm, r.c, tab);
+      }
+      s = warp_sum(s);
+      if (lane == 0) __stcg(p.sum + row * p.nchunk + chunk, s);
+    }
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 4) finish_kernel(const __grid_constant__ SampleParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem);
+  if (threadIdx.x < kTab) sh.tab[threadIdx.x] = exp2((double)threadIdx.x / kTab);
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  __syncthreads();
+  finish_row<BF16>(p, sh, blockIdx.x);
+}
+
+// Has this block brought the row's last segment?  (Block-uniform.)
+__device__ __forceinline__ bool last_segment(int* count, int nseg) {
+  __shared__ int arrived;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) arrived = atomicAdd(count, 1);
+  __syncthreads();
+  const bool last = arrived == nseg - 1;
+  if (last) __threadfence();
+  __syncthreads();
+  return last;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const __grid_constant__ SampleParams p) {
+  __shared__ double tab[kTab];
+  __shared__ uint32_t lo[kBins], hi[kBins];
+  __shared__ u64 red[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if (tid < kTab) tab[tid] = exp2((double)tid / kTab);
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int64_t units = (int64_t)__ldcg(p.marked) * p.nseg;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int64_t row = __ldcg(p.marked + 1 + unit / p.nseg);
+    const int chunk = (int)(unit % p.nseg) * kWarps + w;
+    for (int i = tid; i < kBins; i += kThreads) lo[i] = hi[i] = 0;
+    __syncthreads();
+    const Rule r = rule_of(p, (int)(row / p.n));
+    RowState st;
+    st.m = __ldcg(&p.st[row].m);
+    st.scale = __ldcg(&p.st[row].scale);
+    if (chunk < p.nchunk) {
+      uint32_t raw[BF16 ? 16 : 32];
+      load_chunk<BF16>(p, row, chunk, raw);
+      float x[32];
+      clean_chunk<BF16>(raw, x);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const u64 wt = (u64)__double2ull_rn(weight(x[e], st.m, r.c, tab) * (double)(1ull << p.shift));
+        if (wt == 0) continue;
+        const int bin = bin_of(x[e], st);
+        const uint32_t l = (uint32_t)wt, old = atomicAdd(&lo[bin], l);
+        const uint32_t h = (uint32_t)(wt >> 32) + (old + l < old ? 1u : 0u);
+        if (h) atomicAdd(&hi[bin], h);
+      }
+    }
+    __syncthreads();
+    u64* hist = p.hist + row * kBins;
+    for (int i = tid; i < kBins; i += kThreads) {
+      const u64 v = ((u64)hi[i] << 32) + lo[i];
+      if (v) atomicAdd(hist + i, v);
+    }
+    if (!last_segment(&p.st[row].weighed, p.nseg)) continue;
+    // the bin in which the weight from the top reaches top_p of all: thread i sums
+    // bins 4 i .. 4 i + 3
+    u64 v[4], s = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = __ldcg(hist + 4 * tid + j);
+      s += v[j];
+    }
+    u64 incl = warp_scan(s);
+    if (lane == 31) red[w] = incl;
+    __syncthreads();
+    u64 total = 0;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < w) incl += red[i];
+      total += red[i];
+    }
+    const double want = (double)r.top_p * (double)total;
+    u64 cum = incl - s;
+    if ((double)cum < want && (double)incl >= want) {  // one thread: all together reach it
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if ((double)(cum + v[j]) >= want) {
+          p.st[row].bin = 4 * tid + j;
+          p.st[row].above = cum;
+          p.st[row].total = total;
+          break;
+        }
+        cum += v[j];
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_constant__ SampleParams p) {
+  constexpr int kDrop = BF16 ? 16 : 0;
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if (tid < kTab) sh.tab[tid] = exp2((double)tid / kTab);
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  __syncthreads();
+  const int64_t units = (int64_t)__ldcg(p.marked) * p.nseg;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int64_t row = __ldcg(p.marked + 1 + unit / p.nseg);
+    const int chunk = (int)(unit % p.nseg) * kWarps + w;
+    const Rule r = rule_of(p, (int)(row / p.n));
+    const double c = r.c;
+    RowState st;
+    st.m = __ldcg(&p.st[row].m);
+    st.scale = __ldcg(&p.st[row].scale);
+    st.bin = __ldcg(&p.st[row].bin);
+    const float m = st.m, cut = min_p_cut(r, m);
+    auto over_cut = [&](float x) { return x >= cut || x == m; };
+    if (chunk < p.nchunk) {
+      uint32_t raw[BF16 ? 16 : 32];
+      load_chunk<BF16>(p, row, chunk, raw);
+      float x[32];
+      clean_chunk<BF16>(raw, x);
+      double s = 0.0;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const int bin = bin_of(x[e], st);
+        if (bin < st.bin && over_cut(x[e])) s += weight(x[e], m, c, sh.tab);
+        const bool in = bin == st.bin && x[e] > -INFINITY;
+        const unsigned b = __ballot_sync(0xffffffffu, in);
+        if (b) {
+          int at = 0;
+          if (lane == __ffs(b) - 1) at = atomicAdd(&p.st[row].listed, __popc(b));
+          at = __shfl_sync(0xffffffffu, at, __ffs(b) - 1) + __popc(b & ((1u << lane) - 1u));
+          if (in && at < kRowList) {
+            __stcg(p.list_x + row * kRowList + at, x[e]);
+            __stcg(p.list_i + row * kRowList + at, chunk * kChunk + chunk_token<BF16>(e));
+          }
+        }
+      }
+      s = warp_sum(s);
+      if (lane == 0) __stcg(p.sum + row * p.nchunk + chunk, s);
+    }
+    if (!last_segment(&p.st[row].bordered, p.nseg)) continue;
+    const int n = __ldcg(&p.st[row].listed);
+    u64 above = __ldcg(&p.st[row].above);
+    const u64 total = __ldcg(&p.st[row].total);
+    if (n > kRowList) {
+      // a bin too full to list (many equal logits): walk the row
+      for (int i = tid; i < p.nsub; i += kThreads) sh.sub[i] = __ldcg(p.sub + row * p.nsub + i);
+      __syncthreads();
+      filtered<BF16>(p, sh, row, r, m, -INFINITY, cut, total);
+      __syncthreads();
+      continue;
+    }
+    // the bin's tokens, in any order
+    for (int i = tid; i < n; i += kThreads) {
+      sh.lval[i / kListCap][i % kListCap] = __ldcg(p.list_x + row * kRowList + i);
+      sh.lidx[i / kListCap][i % kListCap] = __ldcg(p.list_i + row * kRowList + i);
+    }
+    if (tid < kWarps) sh.len[tid] = max(0, min(kListCap, n - tid * kListCap));
+    uint32_t klo = 0xffffffffu, khi = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      const uint32_t k = order_key(sh.lval[i / kListCap][i % kListCap]) >> kDrop;
+      klo = min(klo, k);
+      khi = max(khi, k);
+    }
+    klo = __reduce_min_sync(0xffffffffu, klo);
+    khi = __reduce_max_sync(0xffffffffu, khi);
+    if (lane == 0) sh.red[w] = (u64)klo << 32 | khi;
+    __syncthreads();
+    for (int i = 0; i < kWarps; ++i) {
+      klo = min(klo, (uint32_t)(sh.red[i] >> 32));
+      khi = max(khi, (uint32_t)sh.red[i]);
+    }
+    const Source<BF16> src{p, sh, row, -INFINITY, true};
+    auto key = [](float x, int) { return order_key(x) >> kDrop; };
+    auto fixed = [&](float x) { return (u64)__double2ull_rn(weight(x, m, c, sh.tab) * (double)(1ull << p.shift)); };
+    const double want = (double)r.top_p * (double)total;
+    Border e{klo, INT_MAX, 0};
+    uint32_t t;
+    int ties;
+    if (select<true>(src, sh, key, klo, khi, want, m, c, p.shift, t, above, ties)) {
+      const float xt = BF16 ? key_value(t << 16 | ((t & 0x8000u) ? 0u : 0xffffu)) : key_value(t);
+      e = Border{t, tokens_below(above, fixed(xt), ties, want), ties};
+    }
+    const int tie_end = e.c < e.ties ? tie_limit(src, sh, key, e.t, e.c) : INT_MAX;
+    auto in_bin = [&](float x, int i) {
+      const uint32_t k = order_key(x) >> kDrop;
+      return k > e.t || (k == e.t && i <= tie_end);
+    };
+    // the bin's kept tokens join their chunks
+    __syncthreads();
+    for (int i = tid; i < kThreads; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
+    __syncthreads();
+    src.walk([&](float x, int i, bool in) {
+      if (!in || !in_bin(x, i) || !over_cut(x)) return;
+      const u64 wt = fixed(x);
+      const uint32_t l = (uint32_t)wt, old = atomicAdd(&sh.lo[i / kChunk], l);
+      const uint32_t h = (uint32_t)(wt >> 32) + (old + l < old ? 1u : 0u);
+      if (h) atomicAdd(&sh.hi[i / kChunk], h);
+    });
+    __syncthreads();
+    const double own = tid < p.nchunk ? __ldcg(p.sum + row * p.nchunk + tid) +
+                                            (double)(((u64)sh.hi[tid] << 32) + sh.lo[tid]) / (double)(1ull << p.shift)
+                                      : 0.0;
+    draw<BF16>(p, sh, row, own, m, c, [&](float x, int i) {
+      const int bin = bin_of(x, st);
+      return x > -INFINITY && over_cut(x) && (bin < st.bin || (bin == st.bin && in_bin(x, i)));
+    });
+    __syncthreads();
+  }
+}
+
+struct SamplePlan {
+  int64_t rows;
+  int nseg, nsub, nchunk;
+  size_t sub, sum, marked, st, hist, list_x, list_i, bytes;  // workspace offsets
+};
+SamplePlan plan_sample(int B, int M, int V) {
+  SamplePlan s;
+  s.rows = (int64_t)B * (M + 1);
+  s.nsub = (V + kSub - 1) / kSub;
+  s.nchunk = (V + kChunk - 1) / kChunk;
+  s.nseg = (s.nchunk + kWarps - 1) / kWarps;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += ((size_t)s.rows * bytes + 511) / 256 * 256;
+    return o;
+  };
+  s.sub = take(s.nsub * sizeof(float));
+  s.sum = take(s.nchunk * sizeof(double));
+  s.marked = take(sizeof(int));  // (the rounding holds the count as well)
+  s.st = take(sizeof(RowState));
+  s.hist = take(kBins * sizeof(u64));
+  s.list_x = take(kRowList * sizeof(float));
+  s.list_i = take(kRowList * sizeof(int));
+  s.bytes = at;
   return s;
 }
 
 template <bool BF16>
-struct Row {
-  const void* base;
-  int V;
-  float m;
-  double c;  // log2(e) / T
-  int shift;
-  // NaN counts as -inf (never drawn); -0 as +0
-  __device__ __forceinline__ float at(int i) const {
-    float x;
-    if (BF16)
-      x = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base)[i]);
-    else
-      x = reinterpret_cast<const float*>(base)[i];
-    return x == x ? x + 0.f : -INFINITY;
-  }
-  __device__ __forceinline__ unsigned long long weight(float x) const {
-    if (x == m) return 1ull << shift;
-    if (x == -INFINITY || m == INFINITY) return 0ull;
-    return (unsigned long long)__double2ull_rn(exp2(((double)x - (double)m) * c) * (double)(1ull << shift));
-  }
-};
-
-// One CTA per row.
-template <bool BF16>
-__global__ void __launch_bounds__(kSampleThreads) sample_kernel(const __grid_constant__ SampleParams p) {
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  typedef unsigned long long u64;
-  __shared__ u64 red[kSampleThreads / 32];
-  __shared__ float redf[kSampleThreads / 32];
-  __shared__ u64 seg[kSampleThreads];
-  __shared__ int cnt[kSampleThreads];
-  __shared__ int s_tok;
-  const int64_t row = blockIdx.x;
-  const int b = (int)(row / p.n), tid = threadIdx.x;
-  Row<BF16> r;
-  r.base = BF16 ? (const void*)(reinterpret_cast<const uint16_t*>(p.logits) + row * p.stride)
-                : (const void*)(reinterpret_cast<const float*>(p.logits) + row * p.stride);
-  r.V = p.V;
-  r.shift = p.shift;
-  float mx = -INFINITY;
-  for (int i = tid; i < p.V; i += kSampleThreads) mx = fmaxf(mx, r.at(i));
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  if ((tid & 31) == 0) redf[tid >> 5] = mx;
-  if (tid == 0) s_tok = p.V;
-  __syncthreads();
-  for (int i = 0; i < kSampleThreads / 32; ++i) mx = fmaxf(mx, redf[i]);
-  r.m = mx;
-  if (mx == -INFINITY) {  // no token can be drawn
-    if (tid == 0) {
-      p.token[row] = -1;
-      if (p.logprob) p.logprob[row] = -INFINITY;
-    }
-    return;
-  }
-  const float T = p.temperature[b];
-  const bool greedy = !(T > 0.f);
-  r.c = greedy ? 1.0 : 1.4426950408889634 / (double)T;
-  const int k = greedy ? 1 : (p.top_k ? p.top_k[b] : 0);
-  const float tp = p.top_p ? p.top_p[b] : 1.f, mp = p.min_p ? p.min_p[b] : 0.f;
-
-  uint32_t t = 0;
-  int c = p.V;  // keys above t, and the first c tokens with key t
-  const uint32_t mkey = order_key(mx);
-  if (k > 0 && k < p.V) {
-    u64 above = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t mid = t | (1u << bit);
-      u64 cn = 0;
-      for (int i = tid; i < p.V; i += kSampleThreads) cn += order_key(r.at(i)) >= mid;
-      cn = block_sum(cn, red);
-      if (cn >= (u64)k) t = mid;
-      else above = cn;
-    }
-    u64 cn = 0;
-    for (int i = tid; i < p.V; i += kSampleThreads) cn += order_key(r.at(i)) > t;
-    c = k - (int)block_sum(cn, red);
-  }
-  if (tp < 1.f) {
-    if (!(tp > 0.f)) {
-      t = mkey;
-      c = 1;
-    } else {
-      // mass(lo): weight of the kept tokens with key >= lo, and above it
-      auto mass_above = [&](uint32_t lo) {
-        u64 s = 0;
-        for (int i = tid; i < p.V; i += kSampleThreads) {
-          const float x = r.at(i);
-          if (order_key(x) > lo) s += r.weight(x);
-        }
-        return block_sum(s, red);
-      };
-      auto ties = [&](uint32_t key) {
-        u64 s = 0;
-        for (int i = tid; i < p.V; i += kSampleThreads) s += order_key(r.at(i)) == key;
-        return block_sum(s, red);
-      };
-      const u64 ct = min((u64)c, ties(t));
-      const u64 at = mass_above(t), wt = r.weight(key_value(t));
-      const double pz = (double)tp * (double)(at + ct * wt);
-      uint32_t t2 = t;
-      u64 ct2 = ct, a2 = at;
-      if ((double)at >= pz) {  // the boundary lies above t
-        uint32_t lo = 0;       // largest key with mass(key >= lo) >= pz
-        for (int bit = 31; bit >= 0; --bit) {
-          const uint32_t mid = lo | (1u << bit);
-          if (mid <= t || (double)mass_above(mid - 1) >= pz) lo = mid;
-        }
-        t2 = lo;
-        a2 = mass_above(t2);
-        ct2 = ties(t2);
-      }
-      const u64 w2 = r.weight(key_value(t2));
-      // ties kept while the weight before them is below pz
-      u64 l = 0, h = ct2;
-      while (l < h) {
-        const u64 mid = (l + h) / 2;
-        if ((double)(a2 + mid * w2) < pz) l = mid + 1;
-        else h = mid;
-      }
-      t = t2;
-      c = (int)l;
-    }
-  }
-  if (mp > 0.f) {
-    if (mp > 1.f) {
-      t = mkey;
-      c = 1;
-    } else {
-      const float cut = __double2float_ru((double)mx + log2((double)mp) / r.c);
-      const uint32_t ck = order_key(cut + 0.f);
-      if (ck > t) {
-        t = min(ck, mkey);
-        c = p.V;
-      }
-    }
-  }
-  // the draw, in vocabulary order: thread tid owns a contiguous segment
-  const int per = (p.V + kSampleThreads - 1) / kSampleThreads;
-  const int lo = min(p.V, tid * per), hi = min(p.V, lo + per);
-  const u64 wt = r.weight(key_value(t));
-  u64 s = 0;
-  int nt = 0;
-  for (int i = lo; i < hi; ++i) {
-    const float x = r.at(i);
-    const uint32_t key = order_key(x);
-    if (key > t) s += r.weight(x);
-    nt += key == t;
-  }
-  __syncthreads();
-  seg[tid] = s;
-  cnt[tid] = nt;
-  __syncthreads();
-  u64 before = 0, total = 0;
-  int tb = 0, ta = 0;
-  for (int i = 0; i < kSampleThreads; ++i) {
-    const int kept = max(0, min(cnt[i], c - ta));
-    const u64 w = seg[i] + kept * wt;
-    if (i < tid) {
-      before += w;
-      tb += cnt[i];
-    }
-    total += w;
-    ta += cnt[i];
-  }
-  const double target = (double)p.uniform[row] * (double)total;
-  int found = p.V, last = -1;
-  u64 cum = before;
-  for (int i = lo; i < hi; ++i) {
-    const float x = r.at(i);
-    const uint32_t key = order_key(x);
-    u64 w = 0;
-    if (key > t) w = r.weight(x);
-    else if (key == t && tb++ < c) w = wt;
-    if (w == 0) continue;
-    last = i;
-    cum += w;
-    if (found == p.V && (double)cum > target) found = i;
-  }
-  if (found < p.V) atomicMin(&s_tok, found);
-  __syncthreads();
-  cnt[tid] = last;
-  __syncthreads();
-  if (tid == 0) {
-    int tok = s_tok;
-    if (tok == p.V)
-      for (int i = 0; i < kSampleThreads; ++i) tok = cnt[i] >= 0 ? cnt[i] : tok;
-    const float x = r.at(tok);
-    p.token[row] = tok;
-    if (p.logprob)
-      p.logprob[row] = (float)((x == mx ? 0.0 : ((double)x - (double)mx) * r.c * 0.6931471805599453) -
-                               log((double)total / (double)(1ull << p.shift)));
-  }
+tv_status launch_sample(const SampleParams& p, int sms, cudaStream_t s) {
+  const int smem = (int)sizeof(Shared);
+  cudaError_t e = cudaFuncSetAttribute(finish_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(border_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  auto blocks = [&](int64_t n) { return dim3((unsigned)std::min<int64_t>(n, 4 * (int64_t)sms)); };
+  const int64_t units = p.rows * p.nchunk;
+  tv_status r =
+      launch(stream_kernel<BF16>, blocks((units + kWarps - 1) / kWarps), dim3(kThreads), 0, s, 1, true, p);
+  if (r == TV_OK) r = launch(finish_kernel<BF16>, dim3((unsigned)p.rows), dim3(kThreads), smem, s, 1, true, p);
+  if (r != TV_OK || !p.top_p) return r;
+  r = launch(weigh_kernel<BF16>, blocks(p.rows * p.nseg), dim3(kThreads), 0, s, 1, true, p);
+  if (r == TV_OK) r = launch(border_kernel<BF16>, blocks(p.rows * p.nseg), dim3(kThreads), smem, s, 1, true, p);
+  return r;
 }
 
 }  // namespace
 }  // namespace tv
 
 extern "C" size_t tree_accept_sample_workspace_size(int B, int M, int V) {
-  return B > 0 && M >= 0 && V > 0 ? 16 : 0;
+  return B > 0 && M >= 0 && V > 0 ? tv::plan_sample(B, M, V).bytes : 0;
 }
 
 extern "C" tv_status tree_accept_sample(const void* logits, int logits_type, int64_t logits_stride,
@@ -285,11 +1033,21 @@ extern "C" tv_status tree_accept_sample(const void* logits, int logits_type, int
   if (!workspace || !aligned16(workspace) || workspace_bytes < tree_accept_sample_workspace_size(B, M, V))
     return TV_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int dev = 0, sms = 148;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  const SamplePlan lp = plan_sample(B, M, V);
+  char* ws = static_cast<char*>(workspace);
   SampleParams p;
   p.logits = logits;
   p.stride = logits_stride;
+  p.rows = rows;
   p.V = V;
   p.n = M + 1;
+  p.nseg = lp.nseg;
+  p.nsub = lp.nsub;
+  p.nchunk = lp.nchunk;
   p.uniform = uniform;
   p.temperature = temperature;
   p.top_k = top_k;
@@ -297,9 +1055,16 @@ extern "C" tv_status tree_accept_sample(const void* logits, int logits_type, int
   p.min_p = min_p;
   p.token = token;
   p.logprob = logprob;
+  p.sub = reinterpret_cast<float*>(ws + lp.sub);
+  p.sum = reinterpret_cast<double*>(ws + lp.sum);
+  p.marked = reinterpret_cast<int*>(ws + lp.marked);
+  p.st = reinterpret_cast<RowState*>(ws + lp.st);
+  p.hist = reinterpret_cast<u64*>(ws + lp.hist);
+  p.list_x = reinterpret_cast<float*>(ws + lp.list_x);
+  p.list_i = reinterpret_cast<int*>(ws + lp.list_i);
   p.shift = V <= (1 << 17) ? 46 : 45;
-  auto kern = logits_type == TV_LOGITS_F32 ? sample_kernel<false> : sample_kernel<true>;
-  tv_status r = launch(kern, dim3((unsigned)rows), dim3(kSampleThreads), 0, s, 1, true, p);
+  const tv_status r =
+      logits_type == TV_LOGITS_F32 ? launch_sample<false>(p, sms, s) : launch_sample<true>(p, sms, s);
   if (r != TV_OK) return r;
   return launch_accept_walk(token, draft, parent, depth, anc_mask, status, B, M, max_depth, accept_len, path, bonus,
                             s);
