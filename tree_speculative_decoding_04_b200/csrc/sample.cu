@@ -56,7 +56,7 @@ constexpr int kMaxSubs = kMaxVocab / kSub;
 static_assert(kMaxVocab / kChunk <= kThreads, "one thread per chunk in the finish");
 constexpr int kListCap = 512;            // listed tokens per warp
 constexpr int kBins = 1024;
-constexpr int kTab = 128;
+constexpr int kTab = 32, kTabCopies = 16;
 
 struct RowState;
 
@@ -92,7 +92,7 @@ struct RowState {
 };
 
 struct Shared {
-  double tab[kTab];  // 2^(i / kTab)
+  double tab[kTab * kTabCopies];
   double cs;
   double redd[kWarps];
   u64 red[kWarps];
@@ -113,29 +113,56 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// 2^y for y <= 0: y = n / 128 + r, |r| <= 1/256; 2^r by the first five terms of
-// its series (the next is below 2^-49 of the result), 2^(n / 128) from the table
-// and the exponent field.  0 below 2^-1000 and for NaN.
-__device__ __forceinline__ double pow2(double y, const double* tab) {
-  if (!(y > -1000.0)) return 0.0;
+// The table of 2^(i / 32), in 16 copies: lane l reads copy l % 16, whose two banks
+// no lane of its half-warp shares.
+__device__ __forceinline__ void fill_table(double* tab) {
+  for (int i = threadIdx.x; i < kTab * kTabCopies; i += kThreads) tab[i] = exp2((double)(i / kTabCopies) / kTab);
+}
+
+// 2^(y + bias) for -1000 <= y <= 0: y = n / 32 + r, |r| <= 1/64; 2^r by the first
+// six terms of its series (the next is below 2^-48 of the result), 2^(n / 32) from
+// the table and the exponent field.
+__device__ __forceinline__ double pow2_in_range(double y, const double* tab, int bias) {
   const double magic = 6755399441055744.0;  // 1.5 * 2^52: rounds to an integer
   const double t = fma(y, (double)kTab, magic);
   const int n = __double2loint(t);
   const double r = fma(t - magic, -1.0 / kTab, y);
-  double q = 0.0096181291076284772;  // ln2^4 / 24
+  double q = 0.0013333558146428443;  // ln2^5 / 120
+  q = fma(q, r, 0.0096181291076284772);
   q = fma(q, r, 0.055504108664821580);
   q = fma(q, r, 0.24022650695910071);
   q = fma(q, r, 0.69314718055994531);
-  const double v = tab[n & (kTab - 1)] * fma(q, r, 1.0);
-  return __hiloint2double(__double2hiint(v) + ((n >> 7) << 20), __double2loint(v));
+  const double v = tab[(n & (kTab - 1)) * kTabCopies + (threadIdx.x & (kTabCopies - 1))] * fma(q, r, 1.0);
+  return __hiloint2double(__double2hiint(v) + ((n >> 5) + bias) * (1 << 20), __double2loint(v));
 }
 
-// Weight of logit x relative to the maximum m, c = log2(e) / T.
+// Weight of logit x relative to the maximum m, c = log2(e) / T; 0 below 2^-1000.
 __device__ __forceinline__ double weight(float x, float m, double c, const double* tab) {
   if (x == m) return x == -INFINITY ? 0.0 : 1.0;
   if (x == -INFINITY || m == INFINITY) return 0.0;
-  return pow2(((double)x - (double)m) * c, tab);
+  const double y = ((double)x - (double)m) * c;
+  return y > -1000.0 ? pow2_in_range(y, tab, 0) : 0.0;
 }
+
+// The same without branches, for many tokens of one finite maximum: the exponent
+// is formed in one rounding, the float becomes a double through its bits (zeros
+// and denormals to within 2^-126), and what lies 900 octaves below the maximum
+// counts as if it lay there.
+struct Weigher {
+  double c, off;
+  float far;
+  int bias;
+  __device__ __forceinline__ Weigher(float m, double c_, int bias_) : c(c_), bias(bias_) {
+    off = -(double)m * c_;
+    far = (float)fmax((double)m - 900.0 / c_, -3e38);
+  }
+  __device__ __forceinline__ double operator()(float x, const double* tab) const {
+    const uint32_t b = __float_as_uint(fmaxf(x, far));
+    const double d = __hiloint2double((int)((b & 0x80000000u) | (((b & 0x7fffffffu) >> 3) + 0x38000000u)), (int)(b << 29));
+    const double v = pow2_in_range(fma(d, c, off), tab, bias);
+    return x > -INFINITY ? v : 0.0;
+  }
+};
 
 // NaN counts as -inf (never drawn); -0 as +0
 __device__ __forceinline__ float clean(float x) { return x == x ? x + 0.f : -INFINITY; }
@@ -457,6 +484,61 @@ __device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const R
   int present = 0;
   for (int i = 0; i < kWarps; ++i) present += sh.len[i];
 
+  if (present <= kThreads) {
+    // A short list: thread i takes its i-th token and finds the token's place in the
+    // order, and the weight before it, by comparing with all others.
+    int at = threadIdx.x, lw = 0;
+    while (lw < kWarps - 1 && at >= sh.len[lw]) at -= sh.len[lw++];
+    const bool in = (int)threadIdx.x < present;
+    const float x = in ? sh.lval[lw][at] : -INFINITY;
+    const int idx = in ? sh.lidx[lw][at] : 0;
+    const u64 wx = in ? (u64)__double2ull_rn(weight(x, m, c, sh.tab) * (double)(1ull << p.shift)) : 0ull;
+    float* fx = reinterpret_cast<float*>(sh.cnt);  // [256] logits, [256] weights
+    u64* fw = reinterpret_cast<u64*>(sh.lo);
+    fx[threadIdx.x] = x;
+    fw[threadIdx.x] = wx;
+    __syncthreads();
+    int rank = 0;
+    u64 ahead = 0;
+#pragma unroll 4
+    for (int j = 0; j < present; ++j) {
+      const float y = fx[j];
+      const bool first = y > x || (y == x && j < (int)threadIdx.x);
+      rank += first;
+      ahead += first ? fw[j] : 0ull;
+    }
+    bool kept = in && (r.k == 0 || rank < r.k);
+    if (r.use_p) {
+      u64 s = kept ? wx : 0ull;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      if (lane == 0) sh.red[w] = s;
+      __syncthreads();
+      if (r.k > 0) {
+        base = 0;
+        for (int i = 0; i < kWarps; ++i) base += sh.red[i];
+      }
+      kept = kept && (rank == 0 || (double)ahead < (double)r.top_p * (double)base);
+    }
+    kept = kept && (x >= cut || x == m);
+    const double v = kept ? weight(x, m, c, sh.tab) : 0.0;
+    double total;
+    const double incl = block_scan(v, sh, total);
+    if (threadIdx.x == 0) {
+      sh.found = INT_MAX;
+      sh.last = -1;
+    }
+    __syncthreads();
+    if (v > 0.0) {
+      if (incl > (double)p.uniform[row] * total) atomicMin(&sh.found, (int)threadIdx.x);
+      atomicMax(&sh.last, (int)threadIdx.x);
+    }
+    __syncthreads();
+    if ((int)threadIdx.x == (sh.found != INT_MAX ? sh.found : sh.last))
+      put<BF16>(p, row, idx, (x == m ? 0.0 : ((double)x - (double)m) * c * 0.69314718055994531) - log(total));
+    return;
+  }
+
   // ---------------------------------------------------------------- the kept prefix
   const uint32_t klo = order_key(bound) >> kDrop, khi = mkey >> kDrop;
   Border e{klo, INT_MAX, 0};  // everything present
@@ -693,9 +775,9 @@ __device__ __forceinline__ void clean_chunk(const uint32_t (&raw)[BF16 ? 16 : 32
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) stream_kernel(const __grid_constant__ SampleParams p) {
-  __shared__ double tab[kTab];
+  __shared__ double tab[kTab * kTabCopies];
   const int tid = threadIdx.x, lane = tid & 31;
-  if (tid < kTab) tab[tid] = exp2((double)tid / kTab);
+  fill_table(tab);
   pdl_wait_primary();
   pdl_launch_dependents();
   if (blockIdx.x == 0 && tid == 0) p.marked[0] = 0;
@@ -724,14 +806,9 @@ __global__ void __launch_bounds__(kThreads, 4) stream_kernel(const __grid_consta
       const float cm = key_value(top);
       double s = 0.0;
       if (cm < INFINITY && cm > -INFINITY) {
-        // (far below the maximum 2^-900 stands for the weight)
-        const double off = -(double)cm * r.c;
-        const float far = (float)fmax((double)cm - 900.0 / r.c, -3e38);
+        const Weigher wt(cm, r.c, 0);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const double v = pow2(fma((double)fmaxf(x[e], far), r.c, off), tab);
-          s += x[e] > -INFINITY ? v : 0.0;
-        }
+        for (int e = 0; e < 32; ++e) s += wt(x[e], tab);
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e) s += weight(x[e], cm, r.c, tab);
@@ -746,7 +823,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) finish_kernel(const __grid_constant__ SampleParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
-  if (threadIdx.x < kTab) sh.tab[threadIdx.x] = exp2((double)threadIdx.x / kTab);
+  fill_table(sh.tab);
   pdl_wait_primary();
   pdl_launch_dependents();
   __syncthreads();
@@ -768,18 +845,19 @@ __device__ __forceinline__ bool last_segment(int* count, int nseg) {
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const __grid_constant__ SampleParams p) {
-  __shared__ double tab[kTab];
-  __shared__ uint32_t lo[kBins], hi[kBins];
+  __shared__ double tab[kTab * kTabCopies];
+  // weights in three parts of 16 bits: a segment's 8192 tokens cannot overflow one
+  __shared__ uint32_t part[3][kBins];
   __shared__ u64 red[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  if (tid < kTab) tab[tid] = exp2((double)tid / kTab);
+  fill_table(tab);
   pdl_wait_primary();
   pdl_launch_dependents();
   const int64_t units = (int64_t)__ldcg(p.marked) * p.nseg;
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int64_t row = __ldcg(p.marked + 1 + unit / p.nseg);
     const int chunk = (int)(unit % p.nseg) * kWarps + w;
-    for (int i = tid; i < kBins; i += kThreads) lo[i] = hi[i] = 0;
+    for (int i = tid; i < kBins; i += kThreads) part[0][i] = part[1][i] = part[2][i] = 0;
     __syncthreads();
     const Rule r = rule_of(p, (int)(row / p.n));
     RowState st;
@@ -790,20 +868,23 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const __grid_constan
       load_chunk<BF16>(p, row, chunk, raw);
       float x[32];
       clean_chunk<BF16>(raw, x);
+      const Weigher wt(st.m, r.c, p.shift);
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        const u64 wt = (u64)__double2ull_rn(weight(x[e], st.m, r.c, tab) * (double)(1ull << p.shift));
-        if (wt == 0) continue;
+        // rounded to a whole number of 2^-shift in the mantissa's low bits
+        const double v = st.m < INFINITY ? wt(x[e], tab) : (x[e] == st.m ? (double)(1ull << p.shift) : 0.0);
+        const u64 bits = (u64)__double_as_longlong(v + 4503599627370496.0);
+        const uint32_t p0 = (uint32_t)bits & 0xffffu, p1 = (uint32_t)bits >> 16, p2 = (uint32_t)(bits >> 32) & 0xfffffu;
         const int bin = bin_of(x[e], st);
-        const uint32_t l = (uint32_t)wt, old = atomicAdd(&lo[bin], l);
-        const uint32_t h = (uint32_t)(wt >> 32) + (old + l < old ? 1u : 0u);
-        if (h) atomicAdd(&hi[bin], h);
+        if (p0) atomicAdd(&part[0][bin], p0);
+        if (p1) atomicAdd(&part[1][bin], p1);
+        if (p2) atomicAdd(&part[2][bin], p2);
       }
     }
     __syncthreads();
     u64* hist = p.hist + row * kBins;
     for (int i = tid; i < kBins; i += kThreads) {
-      const u64 v = ((u64)hi[i] << 32) + lo[i];
+      const u64 v = ((u64)part[2][i] << 32) + ((u64)part[1][i] << 16) + part[0][i];
       if (v) atomicAdd(hist + i, v);
     }
     if (!last_segment(&p.st[row].weighed, p.nseg)) continue;
@@ -847,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  if (tid < kTab) sh.tab[tid] = exp2((double)tid / kTab);
+  fill_table(sh.tab);
   pdl_wait_primary();
   pdl_launch_dependents();
   __syncthreads();
@@ -869,10 +950,12 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
       float x[32];
       clean_chunk<BF16>(raw, x);
       double s = 0.0;
+      const Weigher wt(m, c, 0);
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         const int bin = bin_of(x[e], st);
-        if (bin < st.bin && over_cut(x[e])) s += weight(x[e], m, c, sh.tab);
+        const bool sure = bin < st.bin && over_cut(x[e]);  // (never for an infinite maximum: that is bin 0)
+        if (__any_sync(0xffffffffu, sure)) s += sure ? wt(x[e], sh.tab) : 0.0;
         const bool in = bin == st.bin && x[e] > -INFINITY;
         const unsigned b = __ballot_sync(0xffffffffu, in);
         if (b) {
