@@ -24,15 +24,17 @@
 //           and a radix selection over histograms of (count, weight) finds the kept
 //           prefix.  Top-p over the whole vocabulary can keep tens of thousands of
 //           tokens; its rows go through two more launches:
-//   weigh   a histogram of weights over 1/32-octave bins below the row's maximum; the
-//           block that brings a row's last segment finds the bin of the border
-//   border  the weight that each chunk keeps for sure, and a list of the tokens in
-//           the border's bin; the last block of a row settles that bin and draws
+//   weigh   a histogram of the weights, to 2^-16, over 1/32-octave bins below the row's
+//           maximum; the block that brings a row's last segment finds the bins in
+//           which the border must lie (one or two)
+//   border  exact sums: of all tokens, of those that each chunk keeps for sure, and a
+//           list of the tokens in the border's bins; the last block of a row settles
+//           those and draws
 //   walk    tree_accept's acceptance walk, on the drawn tokens
 // Weights are doubles (2^((l - m) log2e / T), relative error below 2^-48: a
 // token's share of a flat vocabulary is 2^-18, and a sum in fp32 would move the
-// borders between tokens by as much).  Histograms hold them as 64-bit fixed-point
-// numbers, and all other sums run in a fixed order, so results do not depend on
+// borders between tokens by as much).  The finish's histograms hold them as 64-bit
+// fixed-point numbers, and all other sums run in a fixed order, so results do not depend on
 // the order of the work.
 //
 // Bound by HBM for large batches (the logits are read once, rows with top-p three
@@ -72,12 +74,14 @@ struct SampleParams {
   int32_t* token;
   float* logprob;
   float* sub;    // [rows][nsub] maxima of 128 tokens
-  double* sum;   // [rows][nchunk] weight of a chunk: all, relative to its maximum, or kept for sure
+  double* sum;   // [rows][nchunk] weight of a chunk relative to its maximum; with top-p: what it keeps for sure
   // rows with top-p over the whole vocabulary
   int* marked;         // [0] how many, [1 + i] their rows
   RowState* st;        // [rows]
-  u64* hist;           // [rows][kBins] weights
-  float* list_x;       // [rows][kRowList] tokens in the border's bin
+  u64* hist;           // [rows][kBins] weights in units of 2^-18 of the bin's top
+  double* all;         // [rows][nchunk] weight of a chunk's tokens
+  double* over;        // [rows][nchunk] of those above the border's bins
+  float* list_x;       // [rows][kRowList] tokens in the border's bins
   int* list_i;
   int shift;     // weight 1 is 2^shift in the histograms
 };
@@ -85,9 +89,9 @@ struct SampleParams {
 constexpr int kRowList = kWarps * kListCap;
 
 struct RowState {
-  u64 above, total;       // weight above the border's bin, of all tokens (fixed point)
   float m, scale;         // maximum; bins per unit of logit
-  int bin, listed;        // the border's bin; tokens in it
+  int bin0, bin1;         // the border's bins, first and last
+  int listed;             // tokens in them
   int weighed, bordered;  // segments that have arrived
 };
 
@@ -119,10 +123,10 @@ __device__ __forceinline__ void fill_table(double* tab) {
   for (int i = threadIdx.x; i < kTab * kTabCopies; i += kThreads) tab[i] = exp2((double)(i / kTabCopies) / kTab);
 }
 
-// 2^(y + bias) for -1000 <= y <= 0: y = n / 32 + r, |r| <= 1/64; 2^r by the first
+// 2^y for -1000 <= y <= 0: y = n / 32 + r, |r| <= 1/64; 2^r by the first
 // six terms of its series (the next is below 2^-48 of the result), 2^(n / 32) from
 // the table and the exponent field.
-__device__ __forceinline__ double pow2_in_range(double y, const double* tab, int bias) {
+__device__ __forceinline__ double pow2_in_range(double y, const double* tab) {
   const double magic = 6755399441055744.0;  // 1.5 * 2^52: rounds to an integer
   const double t = fma(y, (double)kTab, magic);
   const int n = __double2loint(t);
@@ -133,7 +137,7 @@ __device__ __forceinline__ double pow2_in_range(double y, const double* tab, int
   q = fma(q, r, 0.24022650695910071);
   q = fma(q, r, 0.69314718055994531);
   const double v = tab[(n & (kTab - 1)) * kTabCopies + (threadIdx.x & (kTabCopies - 1))] * fma(q, r, 1.0);
-  return __hiloint2double(__double2hiint(v) + ((n >> 5) + bias) * (1 << 20), __double2loint(v));
+  return __hiloint2double(__double2hiint(v) + (n >> 5) * (1 << 20), __double2loint(v));
 }
 
 // Weight of logit x relative to the maximum m, c = log2(e) / T; 0 below 2^-1000.
@@ -141,26 +145,23 @@ __device__ __forceinline__ double weight(float x, float m, double c, const doubl
   if (x == m) return x == -INFINITY ? 0.0 : 1.0;
   if (x == -INFINITY || m == INFINITY) return 0.0;
   const double y = ((double)x - (double)m) * c;
-  return y > -1000.0 ? pow2_in_range(y, tab, 0) : 0.0;
+  return y > -1000.0 ? pow2_in_range(y, tab) : 0.0;
 }
 
 // The same without branches, for many tokens of one finite maximum: the exponent
-// is formed in one rounding, the float becomes a double through its bits (zeros
-// and denormals to within 2^-126), and what lies 900 octaves below the maximum
-// counts as if it lay there.
+// is formed in one rounding, and what lies 900 octaves below the maximum (-inf and
+// NaN among it) counts as if it lay there.
 struct Weigher {
   double c, off;
   float far;
-  int bias;
-  __device__ __forceinline__ Weigher(float m, double c_, int bias_) : c(c_), bias(bias_) {
+  // (not where 900 octaves below the maximum is beyond the finite floats)
+  static __device__ __forceinline__ bool fits(float m, double c) { return m < INFINITY && (double)m - 900.0 / c > -1e38; }
+  __device__ __forceinline__ Weigher(float m, double c_) : c(c_) {
     off = -(double)m * c_;
-    far = (float)fmax((double)m - 900.0 / c_, -3e38);
+    far = (float)((double)m - 900.0 / c_);
   }
   __device__ __forceinline__ double operator()(float x, const double* tab) const {
-    const uint32_t b = __float_as_uint(fmaxf(x, far));
-    const double d = __hiloint2double((int)((b & 0x80000000u) | (((b & 0x7fffffffu) >> 3) + 0x38000000u)), (int)(b << 29));
-    const double v = pow2_in_range(fma(d, c, off), tab, bias);
-    return x > -INFINITY ? v : 0.0;
+    return pow2_in_range(fma((double)fmaxf(x, far), c, off), tab);
   }
 };
 
@@ -195,12 +196,13 @@ __device__ __forceinline__ u64 warp_scan(u64 v) {
   return v;
 }
 
-// 1/32-octave bin of a token below the row's maximum (monotone in x; infinities
-// and NaN of the difference go to the ends).
-__device__ __forceinline__ int bin_of(float x, const RowState& r) {
-  if (x == r.m) return 0;
-  const float d = (r.m - x) * r.scale;
-  return d < (float)(kBins - 1) ? (int)d : kBins - 1;
+// 1/32-octave bin of a token below the row's finite maximum (monotone in x), and
+// where in it the token lies.
+__device__ __forceinline__ int bin_of(float x, float m, float scale, float& frac) {
+  const float d = (m - x) * scale;
+  const int bin = (int)fminf(d, (float)(kBins - 1));
+  frac = d - (float)bin;
+  return bin;
 }
 
 // Settings of a row's sequence.
@@ -454,11 +456,10 @@ __device__ void draw(const SampleParams& p, Shared& sh, int64_t row, double own,
   }
 }
 
-// A row with filters, from the tokens that reach `bound`; base: the weight of all
-// tokens (fixed point), for top-p without top-k.
+// A row with filters, from the tokens that reach `bound`: those of the top k, or all
+// that weigh anything, are among them where there is a top-p.
 template <bool BF16>
-__device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const Rule& r, float m, float bound, float cut,
-                         u64 base) {
+__device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const Rule& r, float m, float bound, float cut) {
   constexpr int kDrop = BF16 ? 16 : 0;  // a bf16's key has 16 bits
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const double c = r.c;
@@ -514,10 +515,8 @@ __device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const R
       for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
       if (lane == 0) sh.red[w] = s;
       __syncthreads();
-      if (r.k > 0) {
-        base = 0;
-        for (int i = 0; i < kWarps; ++i) base += sh.red[i];
-      }
+      u64 base = 0;
+      for (int i = 0; i < kWarps; ++i) base += sh.red[i];
       kept = kept && (rank == 0 || (double)ahead < (double)r.top_p * (double)base);
     }
     kept = kept && (x >= cut || x == m);
@@ -550,20 +549,18 @@ __device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const R
   auto value = [&](uint32_t t) { return BF16 ? key_value(t << 16 | ((t & 0x8000u) ? 0u : 0xffffu)) : key_value(t); };
   auto fixed = [&](float x) { return (u64)__double2ull_rn(weight(x, m, c, sh.tab) * (double)(1ull << p.shift)); };
   if (r.use_p) {
-    if (r.k > 0) {  // the weight of the top k
-      u64 s = 0;
-      src.walk([&](float x, int, bool in) {
-        if (in && order_key(x) >> kDrop >= e.t) s += fixed(x);
-      });
+    u64 s = 0;  // the weight of the top k
+    src.walk([&](float x, int, bool in) {
+      if (in && order_key(x) >> kDrop >= e.t) s += fixed(x);
+    });
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      __syncthreads();
-      if (lane == 0) sh.red[w] = s;
-      __syncthreads();
-      base = 0;
-      for (int i = 0; i < kWarps; ++i) base += sh.red[i];
-      if (e.c < e.ties) base -= (u64)(e.ties - e.c) * fixed(value(e.t));
-    }
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    __syncthreads();
+    if (lane == 0) sh.red[w] = s;
+    __syncthreads();
+    u64 base = 0;
+    for (int i = 0; i < kWarps; ++i) base += sh.red[i];
+    if (e.c < e.ties) base -= (u64)(e.ties - e.c) * fixed(value(e.t));
     const double want = (double)r.top_p * (double)base;
     uint32_t t;
     int ties;
@@ -669,7 +666,7 @@ __device__ void finish_row(const SampleParams& p, Shared& sh, int64_t row) {
     if (tid == 0) put<BF16>(p, row, sh.found2, 0.0);
     return;
   }
-  if (r.k == 0 && r.use_p) {  // on to the weighing
+  if (r.k == 0 && r.use_p && Weigher::fits(m, r.c)) {  // on to the weighing
     u64* h = p.hist + row * kBins;
     for (int i = tid; i < kBins; i += kThreads) __stcg(h + i, 0ull);
     if (tid == 0) {
@@ -728,10 +725,11 @@ __device__ void finish_row(const SampleParams& p, Shared& sh, int64_t row) {
     bound = key_value(lowest + ((uint32_t)sh.found << bits));
   }
   if (!r.use_p) bound = fmaxf(bound, cut);  // (top-p's base holds all of the top k)
-  filtered<BF16>(p, sh, row, r, m, fminf(bound, m), cut, 0);
+  if (m == INFINITY) bound = m;             // (nothing else weighs anything)
+  filtered<BF16>(p, sh, row, r, m, fminf(bound, m), cut);
 }
 
-// A warp's chunk of 1024 logits, cleaned.  Lane's tokens: 32 j + lane (fp32), 64 j +
+// A warp's chunk of 1024 logits.  Lane's tokens: 32 j + lane (fp32), 64 j +
 // 2 lane and the next (bf16); token(e) is the index of x[e] in the chunk, and block
 // s of 128 tokens is x[4 s .. 4 s + 3].
 template <bool BF16>
@@ -767,10 +765,12 @@ __device__ __forceinline__ void load_chunk(const SampleParams& p, int64_t row, i
   }
 }
 template <bool BF16>
-__device__ __forceinline__ void clean_chunk(const uint32_t (&raw)[BF16 ? 16 : 32], float (&x)[32]) {
+__device__ __forceinline__ void unpack_chunk(const uint32_t (&raw)[BF16 ? 16 : 32], float (&x)[32]) {
 #pragma unroll
-  for (int e = 0; e < 32; ++e)
-    x[e] = clean(__uint_as_float(!BF16 ? raw[BF16 ? 0 : e] : ((e & 1) ? raw[BF16 ? e >> 1 : 0] & 0xffff0000u : raw[BF16 ? e >> 1 : 0] << 16)));
+  for (int e = 0; e < 32; ++e) {
+    const uint32_t v = raw[BF16 ? e >> 1 : e];
+    x[e] = __uint_as_float(!BF16 ? v : ((e & 1) ? v & 0xffff0000u : v << 16));
+  }
 }
 
 template <bool BF16>
@@ -791,12 +791,12 @@ __global__ void __launch_bounds__(kThreads, 4) stream_kernel(const __grid_consta
     load_chunk<BF16>(p, row, chunk, raw);
     const Rule r = rule_of(p, (int)(row / p.n));
     float x[32];
-    clean_chunk<BF16>(raw, x);
+    unpack_chunk<BF16>(raw, x);
     uint32_t top = 0, mine = 0;
 #pragma unroll
-    for (int s = 0; s < kChunk / kSub; ++s) {
+    for (int s = 0; s < kChunk / kSub; ++s) {  // (a maximum skips NaN)
       const uint32_t k = __reduce_max_sync(
-          0xffffffffu, order_key(fmaxf(fmaxf(x[4 * s], x[4 * s + 1]), fmaxf(x[4 * s + 2], x[4 * s + 3]))));
+          0xffffffffu, order_key(clean(fmaxf(fmaxf(x[4 * s], x[4 * s + 1]), fmaxf(x[4 * s + 2], x[4 * s + 3])))));
       if (lane == s) mine = k;
       top = max(top, k);
     }
@@ -805,13 +805,13 @@ __global__ void __launch_bounds__(kThreads, 4) stream_kernel(const __grid_consta
     if (r.plain) {
       const float cm = key_value(top);
       double s = 0.0;
-      if (cm < INFINITY && cm > -INFINITY) {
-        const Weigher wt(cm, r.c, 0);
+      if (Weigher::fits(cm, r.c)) {
+        const Weigher wt(cm, r.c);
 #pragma unroll
         for (int e = 0; e < 32; ++e) s += wt(x[e], tab);
       } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) s += weight(x[e], cm, r.c, tab);
+        for (int e = 0; e < 32; ++e) s += weight(clean(x[e]), cm, r.c, tab);
       }
       s = warp_sum(s);
       if (lane == 0) __stcg(p.sum + row * p.nchunk + chunk, s);
@@ -845,55 +845,41 @@ __device__ __forceinline__ bool last_segment(int* count, int nseg) {
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const __grid_constant__ SampleParams p) {
-  __shared__ double tab[kTab * kTabCopies];
-  // weights in three parts of 16 bits: a segment's 8192 tokens cannot overflow one
-  __shared__ uint32_t part[3][kBins];
+  __shared__ uint32_t hist_s[kBins];  // (8192 tokens of at most 2^18 each stay below 2^32)
   __shared__ u64 red[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  fill_table(tab);
   pdl_wait_primary();
   pdl_launch_dependents();
   const int64_t units = (int64_t)__ldcg(p.marked) * p.nseg;
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int64_t row = __ldcg(p.marked + 1 + unit / p.nseg);
     const int chunk = (int)(unit % p.nseg) * kWarps + w;
-    for (int i = tid; i < kBins; i += kThreads) part[0][i] = part[1][i] = part[2][i] = 0;
+    for (int i = tid; i < kBins; i += kThreads) hist_s[i] = 0;
     __syncthreads();
-    const Rule r = rule_of(p, (int)(row / p.n));
-    RowState st;
-    st.m = __ldcg(&p.st[row].m);
-    st.scale = __ldcg(&p.st[row].scale);
+    const float m = __ldcg(&p.st[row].m), scale = __ldcg(&p.st[row].scale);
     if (chunk < p.nchunk) {
       uint32_t raw[BF16 ? 16 : 32];
       load_chunk<BF16>(p, row, chunk, raw);
       float x[32];
-      clean_chunk<BF16>(raw, x);
-      const Weigher wt(st.m, r.c, p.shift);
+      unpack_chunk<BF16>(raw, x);
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        // rounded to a whole number of 2^-shift in the mantissa's low bits
-        const double v = st.m < INFINITY ? wt(x[e], tab) : (x[e] == st.m ? (double)(1ull << p.shift) : 0.0);
-        const u64 bits = (u64)__double_as_longlong(v + 4503599627370496.0);
-        const uint32_t p0 = (uint32_t)bits & 0xffffu, p1 = (uint32_t)bits >> 16, p2 = (uint32_t)(bits >> 32) & 0xfffffu;
-        const int bin = bin_of(x[e], st);
-        if (p0) atomicAdd(&part[0][bin], p0);
-        if (p1) atomicAdd(&part[1][bin], p1);
-        if (p2) atomicAdd(&part[2][bin], p2);
+        float frac;
+        const int bin = bin_of(fmaxf(x[e], -INFINITY), m, scale, frac);
+        const uint32_t v = (uint32_t)fast_exp2(fmaf(frac, -1.f / 32.f, 18.f));
+        if (v) atomicAdd(&hist_s[bin], v);
       }
     }
     __syncthreads();
     u64* hist = p.hist + row * kBins;
-    for (int i = tid; i < kBins; i += kThreads) {
-      const u64 v = ((u64)part[2][i] << 32) + ((u64)part[1][i] << 16) + part[0][i];
-      if (v) atomicAdd(hist + i, v);
-    }
+    for (int i = tid; i < kBins; i += kThreads)
+      if (hist_s[i]) atomicAdd(hist + i, (u64)hist_s[i]);
     if (!last_segment(&p.st[row].weighed, p.nseg)) continue;
-    // the bin in which the weight from the top reaches top_p of all: thread i sums
-    // bins 4 i .. 4 i + 3
+    // thread i sums bins 4 i .. 4 i + 3, in units of 2^-46
     u64 v[4], s = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[j] = __ldcg(hist + 4 * tid + j);
+      v[j] = (u64)((double)__ldcg(hist + 4 * tid + j) * (double)fast_exp2(28.f - (float)(4 * tid + j) / 32.f));
       s += v[j];
     }
     u64 incl = warp_scan(s);
@@ -904,19 +890,19 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const __grid_constan
       if (i < w) incl += red[i];
       total += red[i];
     }
-    const double want = (double)r.top_p * (double)total;
+    // Each weight is good to 2^-16: its 18 bits, the exponent's two fp32 roundings
+    // (of up to 32: 2^-18) and the exponentials'.  The border lies behind the last
+    // bin up to which the sum is surely too small, and not behind the first up to
+    // which it surely suffices.
+    const double want = (double)p.top_p[row / p.n] * (double)total, slack = 1.0 / 16384.0;
+    const double first = want * (1.0 - slack), last = want * (1.0 + slack);
     u64 cum = incl - s;
-    if ((double)cum < want && (double)incl >= want) {  // one thread: all together reach it
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if ((double)(cum + v[j]) >= want) {
-          p.st[row].bin = 4 * tid + j;
-          p.st[row].above = cum;
-          p.st[row].total = total;
-          break;
-        }
-        cum += v[j];
-      }
+    for (int j = 0; j < 4; ++j) {
+      const double c0 = (double)cum, c1 = (double)(cum + v[j]);
+      if (c0 < first && c1 >= first) p.st[row].bin0 = 4 * tid + j;
+      if ((c0 < last && c1 >= last) || (tid == kThreads - 1 && j == 3 && c1 < last)) p.st[row].bin1 = 4 * tid + j;
+      cum += v[j];
     }
     __syncthreads();
   }
@@ -938,106 +924,132 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
     const int chunk = (int)(unit % p.nseg) * kWarps + w;
     const Rule r = rule_of(p, (int)(row / p.n));
     const double c = r.c;
-    RowState st;
-    st.m = __ldcg(&p.st[row].m);
-    st.scale = __ldcg(&p.st[row].scale);
-    st.bin = __ldcg(&p.st[row].bin);
-    const float m = st.m, cut = min_p_cut(r, m);
+    const float m = __ldcg(&p.st[row].m), scale = __ldcg(&p.st[row].scale), cut = min_p_cut(r, m);
+    const int bin0 = __ldcg(&p.st[row].bin0), bin1 = __ldcg(&p.st[row].bin1);
     auto over_cut = [&](float x) { return x >= cut || x == m; };
     if (chunk < p.nchunk) {
       uint32_t raw[BF16 ? 16 : 32];
       load_chunk<BF16>(p, row, chunk, raw);
       float x[32];
-      clean_chunk<BF16>(raw, x);
-      double s = 0.0;
-      const Weigher wt(m, c, 0);
+      unpack_chunk<BF16>(raw, x);
+      double keep = 0.0, over = 0.0, all = 0.0;
+      uint32_t listed = 0;  // bit e: x[e] goes to the list
+      const Weigher wt(m, c);
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        const int bin = bin_of(x[e], st);
-        const bool sure = bin < st.bin && over_cut(x[e]);  // (never for an infinite maximum: that is bin 0)
-        if (__any_sync(0xffffffffu, sure)) s += sure ? wt(x[e], sh.tab) : 0.0;
-        const bool in = bin == st.bin && x[e] > -INFINITY;
-        const unsigned b = __ballot_sync(0xffffffffu, in);
-        if (b) {
-          int at = 0;
-          if (lane == __ffs(b) - 1) at = atomicAdd(&p.st[row].listed, __popc(b));
-          at = __shfl_sync(0xffffffffu, at, __ffs(b) - 1) + __popc(b & ((1u << lane) - 1u));
-          if (in && at < kRowList) {
-            __stcg(p.list_x + row * kRowList + at, x[e]);
+        const float xe = fmaxf(x[e], -INFINITY);
+        float frac;
+        const int bin = bin_of(xe, m, scale, frac);
+        const double v = wt(xe, sh.tab);
+        all += v;
+        over += bin < bin0 ? v : 0.0;
+        if (r.use_m) keep += bin < bin0 && over_cut(xe) ? v : 0.0;
+        listed |= bin >= bin0 && bin <= bin1 && xe > -INFINITY ? 1u << e : 0u;
+      }
+      all = warp_sum(all);
+      over = warp_sum(over);
+      keep = r.use_m ? warp_sum(keep) : over;
+      if (lane == 0) {
+        __stcg(p.all + row * p.nchunk + chunk, all);
+        __stcg(p.over + row * p.nchunk + chunk, over);
+        __stcg(p.sum + row * p.nchunk + chunk, keep);
+      }
+      int mine = __popc(listed), at = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, at, off);
+        if (lane >= off) at += o;
+      }
+      const int count = __shfl_sync(0xffffffffu, at, 31);
+      int first = 0;
+      if (lane == 0 && count) first = atomicAdd(&p.st[row].listed, count);
+      at += __shfl_sync(0xffffffffu, first, 0) - mine;
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if ((listed >> e) & 1u) {
+          if (at < kRowList) {
+            __stcg(p.list_x + row * kRowList + at, clean(x[e]));
             __stcg(p.list_i + row * kRowList + at, chunk * kChunk + chunk_token<BF16>(e));
           }
+          ++at;
         }
-      }
-      s = warp_sum(s);
-      if (lane == 0) __stcg(p.sum + row * p.nchunk + chunk, s);
     }
     if (!last_segment(&p.st[row].bordered, p.nseg)) continue;
     const int n = __ldcg(&p.st[row].listed);
-    u64 above = __ldcg(&p.st[row].above);
-    const u64 total = __ldcg(&p.st[row].total);
-    if (n > kRowList) {
-      // a bin too full to list (many equal logits): walk the row
+    const double unit_w = (double)(1ull << p.shift);
+    double total, sure;
+    block_scan(tid < p.nchunk ? __ldcg(p.all + row * p.nchunk + tid) : 0.0, sh, total);
+    block_scan(tid < p.nchunk ? __ldcg(p.over + row * p.nchunk + tid) : 0.0, sh, sure);
+    const double want = (double)r.top_p * total * unit_w;
+    u64 above = (u64)__double2ull_rn(sure * unit_w);
+    bool settled = n <= kRowList && (double)above < want;
+    Border e{0u, INT_MAX, 0};
+    const Source<BF16> src{p, sh, row, -INFINITY, true};
+    auto key = [](float x, int) { return order_key(x) >> kDrop; };
+    auto fixed = [&](float x) { return (u64)__double2ull_rn(weight(x, m, c, sh.tab) * unit_w); };
+    if (settled) {
+      // the bins' tokens, in any order
+      for (int i = tid; i < n; i += kThreads) {
+        sh.lval[i / kListCap][i % kListCap] = __ldcg(p.list_x + row * kRowList + i);
+        sh.lidx[i / kListCap][i % kListCap] = __ldcg(p.list_i + row * kRowList + i);
+      }
+      if (tid < kWarps) sh.len[tid] = max(0, min(kListCap, n - tid * kListCap));
+      uint32_t klo = 0xffffffffu, khi = 0;
+      __syncthreads();
+      for (int i = tid; i < n; i += kThreads) {
+        const uint32_t k = order_key(sh.lval[i / kListCap][i % kListCap]) >> kDrop;
+        klo = min(klo, k);
+        khi = max(khi, k);
+      }
+      klo = __reduce_min_sync(0xffffffffu, klo);
+      khi = __reduce_max_sync(0xffffffffu, khi);
+      if (lane == 0) sh.red[w] = (u64)klo << 32 | khi;
+      __syncthreads();
+      for (int i = 0; i < kWarps; ++i) {
+        klo = min(klo, (uint32_t)(sh.red[i] >> 32));
+        khi = max(khi, (uint32_t)sh.red[i]);
+      }
+      uint32_t t;
+      int ties;
+      settled = n > 0 && select<true>(src, sh, key, klo, khi, want, m, c, p.shift, t, above, ties);
+      if (settled) {
+        const float xt = BF16 ? key_value(t << 16 | ((t & 0x8000u) ? 0u : 0xffffu)) : key_value(t);
+        e = Border{t, tokens_below(above, fixed(xt), ties, want), ties};
+      }
+    }
+    if (!settled) {
+      // the bins hold too many tokens to list (equal logits, or a top_p so close to 1
+      // that the border is among the lightest): walk the row
       for (int i = tid; i < p.nsub; i += kThreads) sh.sub[i] = __ldcg(p.sub + row * p.nsub + i);
       __syncthreads();
-      filtered<BF16>(p, sh, row, r, m, -INFINITY, cut, total);
+      filtered<BF16>(p, sh, row, r, m, -INFINITY, cut);
       __syncthreads();
       continue;
     }
-    // the bin's tokens, in any order
-    for (int i = tid; i < n; i += kThreads) {
-      sh.lval[i / kListCap][i % kListCap] = __ldcg(p.list_x + row * kRowList + i);
-      sh.lidx[i / kListCap][i % kListCap] = __ldcg(p.list_i + row * kRowList + i);
-    }
-    if (tid < kWarps) sh.len[tid] = max(0, min(kListCap, n - tid * kListCap));
-    uint32_t klo = 0xffffffffu, khi = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-      const uint32_t k = order_key(sh.lval[i / kListCap][i % kListCap]) >> kDrop;
-      klo = min(klo, k);
-      khi = max(khi, k);
-    }
-    klo = __reduce_min_sync(0xffffffffu, klo);
-    khi = __reduce_max_sync(0xffffffffu, khi);
-    if (lane == 0) sh.red[w] = (u64)klo << 32 | khi;
-    __syncthreads();
-    for (int i = 0; i < kWarps; ++i) {
-      klo = min(klo, (uint32_t)(sh.red[i] >> 32));
-      khi = max(khi, (uint32_t)sh.red[i]);
-    }
-    const Source<BF16> src{p, sh, row, -INFINITY, true};
-    auto key = [](float x, int) { return order_key(x) >> kDrop; };
-    auto fixed = [&](float x) { return (u64)__double2ull_rn(weight(x, m, c, sh.tab) * (double)(1ull << p.shift)); };
-    const double want = (double)r.top_p * (double)total;
-    Border e{klo, INT_MAX, 0};
-    uint32_t t;
-    int ties;
-    if (select<true>(src, sh, key, klo, khi, want, m, c, p.shift, t, above, ties)) {
-      const float xt = BF16 ? key_value(t << 16 | ((t & 0x8000u) ? 0u : 0xffffu)) : key_value(t);
-      e = Border{t, tokens_below(above, fixed(xt), ties, want), ties};
-    }
     const int tie_end = e.c < e.ties ? tie_limit(src, sh, key, e.t, e.c) : INT_MAX;
-    auto in_bin = [&](float x, int i) {
+    auto in_bins = [&](float x, int i) {
       const uint32_t k = order_key(x) >> kDrop;
       return k > e.t || (k == e.t && i <= tie_end);
     };
-    // the bin's kept tokens join their chunks
+    // the bins' kept tokens join their chunks
     __syncthreads();
-    for (int i = tid; i < kThreads; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
+    sh.lo[tid] = sh.hi[tid] = 0;
     __syncthreads();
     src.walk([&](float x, int i, bool in) {
-      if (!in || !in_bin(x, i) || !over_cut(x)) return;
-      const u64 wt = fixed(x);
-      const uint32_t l = (uint32_t)wt, old = atomicAdd(&sh.lo[i / kChunk], l);
-      const uint32_t h = (uint32_t)(wt >> 32) + (old + l < old ? 1u : 0u);
+      if (!in || !in_bins(x, i) || !over_cut(x)) return;
+      const u64 v = fixed(x);
+      const uint32_t l = (uint32_t)v, old = atomicAdd(&sh.lo[i / kChunk], l);
+      const uint32_t h = (uint32_t)(v >> 32) + (old + l < old ? 1u : 0u);
       if (h) atomicAdd(&sh.hi[i / kChunk], h);
     });
     __syncthreads();
     const double own = tid < p.nchunk ? __ldcg(p.sum + row * p.nchunk + tid) +
-                                            (double)(((u64)sh.hi[tid] << 32) + sh.lo[tid]) / (double)(1ull << p.shift)
+                                            (double)(((u64)sh.hi[tid] << 32) + sh.lo[tid]) / unit_w
                                       : 0.0;
     draw<BF16>(p, sh, row, own, m, c, [&](float x, int i) {
-      const int bin = bin_of(x, st);
-      return x > -INFINITY && over_cut(x) && (bin < st.bin || (bin == st.bin && in_bin(x, i)));
+      float frac;
+      const int bin = bin_of(x, m, scale, frac);
+      return x > -INFINITY && over_cut(x) && (bin < bin0 || (bin <= bin1 && in_bins(x, i)));
     });
     __syncthreads();
   }
@@ -1046,7 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
 struct SamplePlan {
   int64_t rows;
   int nseg, nsub, nchunk;
-  size_t sub, sum, marked, st, hist, list_x, list_i, bytes;  // workspace offsets
+  size_t sub, sum, all, over, marked, st, hist, list_x, list_i, bytes;  // workspace offsets
 };
 SamplePlan plan_sample(int B, int M, int V) {
   SamplePlan s;
@@ -1062,6 +1074,8 @@ SamplePlan plan_sample(int B, int M, int V) {
   };
   s.sub = take(s.nsub * sizeof(float));
   s.sum = take(s.nchunk * sizeof(double));
+  s.all = take(s.nchunk * sizeof(double));
+  s.over = take(s.nchunk * sizeof(double));
   s.marked = take(sizeof(int));  // (the rounding holds the count as well)
   s.st = take(sizeof(RowState));
   s.hist = take(kBins * sizeof(u64));
@@ -1140,6 +1154,8 @@ extern "C" tv_status tree_accept_sample(const void* logits, int logits_type, int
   p.logprob = logprob;
   p.sub = reinterpret_cast<float*>(ws + lp.sub);
   p.sum = reinterpret_cast<double*>(ws + lp.sum);
+  p.all = reinterpret_cast<double*>(ws + lp.all);
+  p.over = reinterpret_cast<double*>(ws + lp.over);
   p.marked = reinterpret_cast<int*>(ws + lp.marked);
   p.st = reinterpret_cast<RowState*>(ws + lp.st);
   p.hist = reinterpret_cast<u64*>(ws + lp.hist);
