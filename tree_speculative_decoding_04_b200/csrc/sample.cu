@@ -14,22 +14,24 @@
 // Launches, each over the whole GPU:
 //   stream  one pass over the logits (a chunk of 1024 per warp, loads of 128 bytes
 //           that need no alignment): the maximum of every 128 tokens and, for rows
-//           without a filter, each chunk's weight relative to its maximum
+//           that need the weight of all tokens, each chunk's weight relative to its
+//           maximum
 //   finish  a block per row.  No filter: the chunk in which the target falls is
-//           read again.  Top-k, min-p: no token below a bound can be kept or matter
+//           read again.  Filters: no token below a bound can be kept or matter
 //           (top-k: the k-th largest of the 128-token maxima bounds the k-th largest
-//           token; min-p: its threshold), so only 128-token blocks that reach it are
+//           token; top-p: once these maxima alone weigh enough, so do the tokens above
+//           them; min-p: its threshold), so only 128-token blocks that reach it are
 //           read again; the tokens that do go to a list in shared memory, in
 //           vocabulary order (were it to overflow, they are walked in L2 instead),
 //           and a radix selection over histograms of (count, weight) finds the kept
-//           prefix.  Top-p over the whole vocabulary can keep tens of thousands of
-//           tokens; its rows go through two more launches:
+//           prefix; up to 256 tokens are simply compared with each other.  Rows whose
+//           top-p keeps too many tokens for this go through two more launches:
 //   weigh   a histogram of the weights, to 2^-16, over 1/32-octave bins below the row's
 //           maximum; the block that brings a row's last segment finds the bins in
 //           which the border must lie (one or two)
-//   border  exact sums: of all tokens, of those that each chunk keeps for sure, and a
-//           list of the tokens in the border's bins; the last block of a row settles
-//           those and draws
+//   border  exact sums of the tokens that each chunk keeps for sure, and a list of the
+//           tokens in the border's bins; the last block of a row settles those and
+//           draws
 //   walk    tree_accept's acceptance walk, on the drawn tokens
 // Weights are doubles (2^((l - m) log2e / T), relative error below 2^-48: a
 // token's share of a flat vocabulary is 2^-18, and a sum in fp32 would move the
@@ -56,7 +58,7 @@ constexpr int kSub = 128;                // tokens per recorded maximum
 constexpr int kMaxVocab = 1 << 18;       // fixed-point weights of one row stay below 2^63
 constexpr int kMaxSubs = kMaxVocab / kSub;
 static_assert(kMaxVocab / kChunk <= kThreads, "one thread per chunk in the finish");
-constexpr int kListCap = 512;            // listed tokens per warp
+constexpr int kListCap = 384;            // listed tokens per warp
 constexpr int kBins = 1024;
 constexpr int kTab = 32, kTabCopies = 16;
 
@@ -74,13 +76,12 @@ struct SampleParams {
   int32_t* token;
   float* logprob;
   float* sub;    // [rows][nsub] maxima of 128 tokens
-  double* sum;   // [rows][nchunk] weight of a chunk relative to its maximum; with top-p: what it keeps for sure
-  // rows with top-p over the whole vocabulary
+  double* sum;   // [rows][nchunk] weight of a chunk relative to its maximum; after border: what it keeps for sure
+  // rows whose top-p keeps many tokens
   int* marked;         // [0] how many, [1 + i] their rows
   RowState* st;        // [rows]
   u64* hist;           // [rows][kBins] weights in units of 2^-18 of the bin's top
-  double* all;         // [rows][nchunk] weight of a chunk's tokens
-  double* over;        // [rows][nchunk] of those above the border's bins
+  double* over;        // [rows][nchunk] weight of a chunk's tokens above the border's bins
   float* list_x;       // [rows][kRowList] tokens in the border's bins
   int* list_i;
   int shift;     // weight 1 is 2^shift in the histograms
@@ -89,6 +90,7 @@ struct SampleParams {
 constexpr int kRowList = kWarps * kListCap;
 
 struct RowState {
+  double total;           // weight of all tokens
   float m, scale;         // maximum; bins per unit of logit
   int bin0, bin1;         // the border's bins, first and last
   int listed;             // tokens in them
@@ -104,6 +106,7 @@ struct Shared {
   uint32_t cnt[kBins], lo[kBins], hi[kBins];
   float lval[kWarps][kListCap];
   int lidx[kWarps][kListCap];
+  uint16_t blk[kWarps][kMaxSubs / kWarps + 32];  // 128-token blocks that a warp reads
   int len[kWarps];
   int found, found2, last, last2;
   u64 found_mass;
@@ -209,7 +212,7 @@ __device__ __forceinline__ int bin_of(float x, float m, float scale, float& frac
 struct Rule {
   float T, top_p, min_p;
   int k;  // 0: off
-  bool greedy, use_p, use_m, plain;  // plain: no filter
+  bool greedy, use_p, use_m, plain, need_total;  // plain: no filter
   double c;  // log2(e) / T
 };
 __device__ __forceinline__ Rule rule_of(const SampleParams& p, int b) {
@@ -224,6 +227,7 @@ __device__ __forceinline__ Rule rule_of(const SampleParams& p, int b) {
   r.use_p = r.top_p < 1.f;  // false for NaN
   r.use_m = r.min_p > 0.f;
   r.plain = !r.greedy && r.k == 0 && !r.use_p && !r.use_m;
+  r.need_total = r.plain || (!r.greedy && r.k == 0 && r.use_p);
   return r;
 }
 
@@ -242,26 +246,31 @@ struct Source {
   __device__ __forceinline__ void blocks(F f) const {  // f(first token, x[4]) for each of the warp's blocks
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b0 = (int)((int64_t)p.nsub * w / kWarps), b1 = (int)((int64_t)p.nsub * (w + 1) / kWarps);
+    int n = 0;
     for (int base = b0; base < b1; base += 32) {
-      unsigned m = __ballot_sync(0xffffffffu, base + lane < b1 && sh.sub[min(base + lane, b1 - 1)] >= bound);
-      while (m) {
-        int blk[4];
-        float x[4][4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {  // four blocks' loads in flight
-          blk[k] = m ? base + __ffs(m) - 1 : -1;
-          m &= m - 1;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int i = blk[k] * kSub + j * 32 + lane;
-            x[k][j] = blk[k] >= 0 && i < p.V ? logit<BF16>(p, row, i) : -INFINITY;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (blk[k] >= 0) f(blk[k] * kSub, x[k]);
-      }
+      const bool in = base + lane < b1 && sh.sub[min(base + lane, b1 - 1)] >= bound;
+      const unsigned m = __ballot_sync(0xffffffffu, in);
+      if (in) sh.blk[w][n + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(base + lane);
+      n += __popc(m);
     }
+    __syncwarp();
+    for (int k0 = 0; k0 < n; k0 += 4) {  // four blocks' loads in flight
+      float x[4][4];
+      int first[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        first[k] = k0 + k < n ? sh.blk[w][k0 + k] * kSub : p.V;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = first[k] + j * 32 + lane;
+          x[k][j] = i < p.V ? logit<BF16>(p, row, i) : -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (first[k] < p.V) f(first[k], x[k]);
+    }
+    __syncwarp();
   }
   template <class F>
   __device__ __forceinline__ void walk(F f) const {  // f(x, index, present), warp-collective
@@ -280,6 +289,16 @@ struct Source {
   }
 };
 
+// The maxima of the 128-token blocks, for select().
+struct Maxima {
+  const SampleParams& p;
+  Shared& sh;
+  template <class F>
+  __device__ __forceinline__ void walk(F f) const {
+    for (int i = threadIdx.x; i < p.nsub; i += kThreads) f(sh.sub[i], i, true);
+  }
+};
+
 // A border of the order: keys above t, and the first c of the `ties` tokens with key t.
 struct Border {
   uint32_t t;
@@ -290,8 +309,9 @@ struct Border {
 // false) or first weigh `want` (MASS), by histograms over ever narrower key
 // ranges.  key(x, index): keys outside the range are left out.  above: the count
 // or weight above `hi` on entry, above the found key on return; ties: tokens with
-// that key.  False if all tokens together do not reach it.
-template <bool MASS, class Src, class Key>
+// that key.  False if all tokens together do not reach it.  COARSE: one histogram;
+// t is the lower end of the range that holds the key.
+template <bool MASS, bool COARSE = false, class Src, class Key>
 __device__ bool select(const Src& src, Shared& sh, Key key, uint32_t lo, uint32_t hi, double want, float m, double c,
                        int shift, uint32_t& t, u64& above, int& ties) {
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -348,7 +368,7 @@ __device__ bool select(const Src& src, Shared& sh, Key key, uint32_t lo, uint32_
     above = sh.found_mass;
     ties = (int)sh.cnt[bin];
     lo += (uint32_t)bin << sh_bits;
-    if (sh_bits == 0) break;
+    if (COARSE || sh_bits == 0) break;
     hi = min(hi, lo + ((1u << sh_bits) - 1u));
   }
   t = lo;
@@ -456,10 +476,12 @@ __device__ void draw(const SampleParams& p, Shared& sh, int64_t row, double own,
   }
 }
 
-// A row with filters, from the tokens that reach `bound`: those of the top k, or all
-// that weigh anything, are among them where there is a top-p.
-template <bool BF16>
-__device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const Rule& r, float m, float bound, float cut) {
+// A row with filters, from the tokens that reach `bound`.  total: the weight of all
+// tokens, for top-p without top-k.  LIST: false is returned where the list
+// overflows.
+template <bool BF16, bool LIST>
+__device__ bool filtered(const SampleParams& p, Shared& sh, int64_t row, const Rule& r, float m, float bound, float cut,
+                         double total) {
   constexpr int kDrop = BF16 ? 16 : 0;  // a bf16's key has 16 bits
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const double c = r.c;
@@ -482,6 +504,7 @@ __device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const R
   });
   if (lane == 0) sh.len[w] = len;
   src.listed = __syncthreads_and(len <= kListCap) != 0;
+  if (LIST && !src.listed) return false;
   int present = 0;
   for (int i = 0; i < kWarps; ++i) present += sh.len[i];
 
@@ -515,13 +538,16 @@ __device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const R
       for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
       if (lane == 0) sh.red[w] = s;
       __syncthreads();
-      u64 base = 0;
-      for (int i = 0; i < kWarps; ++i) base += sh.red[i];
-      kept = kept && (rank == 0 || (double)ahead < (double)r.top_p * (double)base);
+      double base = total * (double)(1ull << p.shift);
+      if (r.k > 0) {
+        u64 all = 0;
+        for (int i = 0; i < kWarps; ++i) all += sh.red[i];
+        base = (double)all;
+      }
+      kept = kept && (rank == 0 || (double)ahead < (double)r.top_p * base);
     }
     kept = kept && (x >= cut || x == m);
     const double v = kept ? weight(x, m, c, sh.tab) : 0.0;
-    double total;
     const double incl = block_scan(v, sh, total);
     if (threadIdx.x == 0) {
       sh.found = INT_MAX;
@@ -535,7 +561,7 @@ __device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const R
     __syncthreads();
     if ((int)threadIdx.x == (sh.found != INT_MAX ? sh.found : sh.last))
       put<BF16>(p, row, idx, (x == m ? 0.0 : ((double)x - (double)m) * c * 0.69314718055994531) - log(total));
-    return;
+    return true;
   }
 
   // ---------------------------------------------------------------- the kept prefix
@@ -549,19 +575,23 @@ __device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const R
   auto value = [&](uint32_t t) { return BF16 ? key_value(t << 16 | ((t & 0x8000u) ? 0u : 0xffffu)) : key_value(t); };
   auto fixed = [&](float x) { return (u64)__double2ull_rn(weight(x, m, c, sh.tab) * (double)(1ull << p.shift)); };
   if (r.use_p) {
-    u64 s = 0;  // the weight of the top k
-    src.walk([&](float x, int, bool in) {
-      if (in && order_key(x) >> kDrop >= e.t) s += fixed(x);
-    });
+    double base = total * (double)(1ull << p.shift);
+    if (r.k > 0) {  // the weight of the top k
+      u64 s = 0;
+      src.walk([&](float x, int, bool in) {
+        if (in && order_key(x) >> kDrop >= e.t) s += fixed(x);
+      });
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    __syncthreads();
-    if (lane == 0) sh.red[w] = s;
-    __syncthreads();
-    u64 base = 0;
-    for (int i = 0; i < kWarps; ++i) base += sh.red[i];
-    if (e.c < e.ties) base -= (u64)(e.ties - e.c) * fixed(value(e.t));
-    const double want = (double)r.top_p * (double)base;
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      __syncthreads();
+      if (lane == 0) sh.red[w] = s;
+      __syncthreads();
+      u64 all = 0;
+      for (int i = 0; i < kWarps; ++i) all += sh.red[i];
+      if (e.c < e.ties) all -= (u64)(e.ties - e.c) * fixed(value(e.t));
+      base = (double)all;
+    }
+    const double want = (double)r.top_p * base;
     uint32_t t;
     int ties;
     u64 above = 0;
@@ -585,7 +615,7 @@ __device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const R
   __syncthreads();
   if (lane == 0) sh.redd[w] = s;
   __syncthreads();
-  double total = 0.0;
+  total = 0.0;
   for (int i = 0; i < kWarps; ++i) total += sh.redd[i];
   const double target = (double)p.uniform[row] * total;
   int owner = -1, last_w = 0;
@@ -626,6 +656,7 @@ __device__ void filtered(const SampleParams& p, Shared& sh, int64_t row, const R
     if (lane == 0)
       put<BF16>(p, row, tok, (tx == m ? 0.0 : ((double)tx - (double)m) * c * 0.69314718055994531) - log(total));
   }
+  return true;
 }
 
 __device__ __forceinline__ float min_p_cut(const Rule& r, float m) {
@@ -666,67 +697,59 @@ __device__ void finish_row(const SampleParams& p, Shared& sh, int64_t row) {
     if (tid == 0) put<BF16>(p, row, sh.found2, 0.0);
     return;
   }
-  if (r.k == 0 && r.use_p && Weigher::fits(m, r.c)) {  // on to the weighing
-    u64* h = p.hist + row * kBins;
-    for (int i = tid; i < kBins; i += kThreads) __stcg(h + i, 0ull);
-    if (tid == 0) {
-      RowState st = {};
-      st.m = m;
-      st.scale = (float)fmin(32.0 * r.c, 3e38);
-      p.st[row] = st;
-      p.marked[1 + atomicAdd(p.marked, 1)] = (int)row;
-    }
-    return;
-  }
-  if (r.plain) {
-    double own = 0.0;
+  double own = 0.0, total = 0.0;
+  if (r.need_total) {
     if (tid < p.nchunk) {
       float cm = -INFINITY;
       for (int i = tid * (kChunk / kSub); i < min(p.nsub, (tid + 1) * (kChunk / kSub)); ++i) cm = fmaxf(cm, sh.sub[i]);
       own = __ldcg(p.sum + row * p.nchunk + tid) * weight(cm, m, r.c, sh.tab);
     }
-    draw<BF16>(p, sh, row, own, m, r.c, [](float, int) { return true; });
-    return;
+    if (r.plain) {
+      draw<BF16>(p, sh, row, own, m, r.c, [](float, int) { return true; });
+      return;
+    }
+    block_scan(own, sh, total);
   }
   const float cut = min_p_cut(r, m);
   float bound = -INFINITY;
+  const Maxima maxima{p, sh};
+  auto key = [](float x, int) { return order_key(x); };
+  uint32_t lowest = 0xffffffffu, t;
+  for (int i = tid; i < p.nsub; i += kThreads) lowest = min(lowest, order_key(sh.sub[i]));
+  lowest = __reduce_min_sync(0xffffffffu, lowest);
+  __syncthreads();
+  if (lane == 0) sh.red[w] = lowest;
+  __syncthreads();
+  for (int i = 0; i < kWarps; ++i) lowest = min(lowest, (uint32_t)sh.red[i]);
+  u64 above = 0;
+  int ties;
   if (r.k > 0 && r.k <= p.nsub) {
-    // a value that at least k of the 128-token maxima reach
-    uint32_t lowest = 0xffffffffu;
-    for (int i = tid; i < p.nsub; i += kThreads) lowest = min(lowest, order_key(sh.sub[i]));
-    lowest = __reduce_min_sync(0xffffffffu, lowest);
-    __syncthreads();
-    if (lane == 0) sh.red[w] = lowest;
-    for (int i = tid; i < kBins; i += kThreads) sh.cnt[i] = 0;
-    __syncthreads();
-    for (int i = 0; i < kWarps; ++i) lowest = min(lowest, (uint32_t)sh.red[i]);
-    const int bits = max(0, 32 - __clz(mkey - lowest) - 10);
-    for (int i = tid; i < p.nsub; i += kThreads) atomicAdd(&sh.cnt[(order_key(sh.sub[i]) - lowest) >> bits], 1u);
-    __syncthreads();
-    u64 s = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s += sh.cnt[kBins - 1 - 4 * tid - j];
-    u64 in = warp_scan(s);
-    __syncthreads();
-    if (lane == 31) sh.red[w] = in;
-    __syncthreads();
-    for (int i = 0; i < w; ++i) in += sh.red[i];
-    if (in >= (u64)r.k && in - s < (u64)r.k) {
-      u64 cum = in - s;
-      for (int j = 0; j < 4; ++j) {
-        cum += sh.cnt[kBins - 1 - 4 * tid - j];
-        if (cum >= (u64)r.k) {
-          sh.found = kBins - 1 - 4 * tid - j;
-          break;
-        }
+    // a value that at least k of the maxima reach
+    if (select<false, true>(maxima, sh, key, lowest, mkey, (double)r.k, m, r.c, p.shift, t, above, ties)) bound = key_value(t);
+  } else if (r.k == 0 && r.use_p) {
+    // a value such that the maxima that reach it weigh top_p of all (2^-40 is more
+    // than the sums' errors)
+    const double want = (double)r.top_p * total * (double)(1ull << p.shift) * (1.0 + 1e-12);
+    const bool few =
+        select<true, true>(maxima, sh, key, lowest, mkey, want, m, r.c, p.shift, t, above, ties) &&
+        filtered<BF16, true>(p, sh, row, r, m, key_value(t), cut, total);
+    if (few) return;
+    if (Weigher::fits(m, r.c)) {  // on to the weighing
+      u64* h = p.hist + row * kBins;
+      for (int i = tid; i < kBins; i += kThreads) __stcg(h + i, 0ull);
+      if (tid == 0) {
+        RowState st = {};
+        st.total = total;
+        st.m = m;
+        st.scale = (float)fmin(32.0 * r.c, 3e38);
+        p.st[row] = st;
+        p.marked[1 + atomicAdd(p.marked, 1)] = (int)row;
       }
+      return;
     }
-    __syncthreads();
-    bound = key_value(lowest + ((uint32_t)sh.found << bits));
   }
   if (!r.use_p) bound = fmaxf(bound, cut);  // (top-p's base holds all of the top k)
-  if (m == INFINITY) bound = m;             // (nothing else weighs anything)
-  filtered<BF16>(p, sh, row, r, m, fminf(bound, m), cut);
+  filtered<BF16, false>(p, sh, row, r, m, fminf(bound, m), cut, total);
 }
 
 // A warp's chunk of 1024 logits.  Lane's tokens: 32 j + lane (fp32), 64 j +
@@ -802,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 4) stream_kernel(const __grid_consta
     }
     const int sub0 = chunk * (kChunk / kSub);
     if (lane < kChunk / kSub && sub0 + lane < p.nsub) __stcg(p.sub + row * p.nsub + sub0 + lane, key_value(mine));
-    if (r.plain) {
+    if (r.need_total) {
       const float cm = key_value(top);
       double s = 0.0;
       if (Weigher::fits(cm, r.c)) {
@@ -885,22 +908,18 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const __grid_constan
     u64 incl = warp_scan(s);
     if (lane == 31) red[w] = incl;
     __syncthreads();
-    u64 total = 0;
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < w) incl += red[i];
-      total += red[i];
-    }
+    for (int i = 0; i < w; ++i) incl += red[i];
     // Each weight is good to 2^-16: its 18 bits, the exponent's two fp32 roundings
     // (of up to 32: 2^-18) and the exponentials'.  The border lies behind the last
     // bin up to which the sum is surely too small, and not behind the first up to
     // which it surely suffices.
-    const double want = (double)p.top_p[row / p.n] * (double)total, slack = 1.0 / 16384.0;
+    const double want = (double)p.top_p[row / p.n] * __ldcg(&p.st[row].total) * 70368744177664.0, slack = 1.0 / 16384.0;
     const double first = want * (1.0 - slack), last = want * (1.0 + slack);
     u64 cum = incl - s;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const double c0 = (double)cum, c1 = (double)(cum + v[j]);
-      if (c0 < first && c1 >= first) p.st[row].bin0 = 4 * tid + j;
+      if ((c0 < first && c1 >= first) || (tid == kThreads - 1 && j == 3 && c1 < first)) p.st[row].bin0 = 4 * tid + j;
       if ((c0 < last && c1 >= last) || (tid == kThreads - 1 && j == 3 && c1 < last)) p.st[row].bin1 = 4 * tid + j;
       cum += v[j];
     }
@@ -932,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
       load_chunk<BF16>(p, row, chunk, raw);
       float x[32];
       unpack_chunk<BF16>(raw, x);
-      double keep = 0.0, over = 0.0, all = 0.0;
+      double keep = 0.0, over = 0.0;
       uint32_t listed = 0;  // bit e: x[e] goes to the list
       const Weigher wt(m, c);
 #pragma unroll
@@ -940,17 +959,16 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
         const float xe = fmaxf(x[e], -INFINITY);
         float frac;
         const int bin = bin_of(xe, m, scale, frac);
-        const double v = wt(xe, sh.tab);
-        all += v;
-        over += bin < bin0 ? v : 0.0;
-        if (r.use_m) keep += bin < bin0 && over_cut(xe) ? v : 0.0;
+        if (__any_sync(0xffffffffu, bin < bin0)) {
+          const double v = bin < bin0 ? wt(xe, sh.tab) : 0.0;
+          over += v;
+          keep += over_cut(xe) ? v : 0.0;
+        }
         listed |= bin >= bin0 && bin <= bin1 && xe > -INFINITY ? 1u << e : 0u;
       }
-      all = warp_sum(all);
       over = warp_sum(over);
-      keep = r.use_m ? warp_sum(keep) : over;
+      keep = warp_sum(keep);
       if (lane == 0) {
-        __stcg(p.all + row * p.nchunk + chunk, all);
         __stcg(p.over + row * p.nchunk + chunk, over);
         __stcg(p.sum + row * p.nchunk + chunk, keep);
       }
@@ -977,8 +995,8 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
     if (!last_segment(&p.st[row].bordered, p.nseg)) continue;
     const int n = __ldcg(&p.st[row].listed);
     const double unit_w = (double)(1ull << p.shift);
-    double total, sure;
-    block_scan(tid < p.nchunk ? __ldcg(p.all + row * p.nchunk + tid) : 0.0, sh, total);
+    const double total = __ldcg(&p.st[row].total);
+    double sure;
     block_scan(tid < p.nchunk ? __ldcg(p.over + row * p.nchunk + tid) : 0.0, sh, sure);
     const double want = (double)r.top_p * total * unit_w;
     u64 above = (u64)__double2ull_rn(sure * unit_w);
@@ -1022,7 +1040,7 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
       // that the border is among the lightest): walk the row
       for (int i = tid; i < p.nsub; i += kThreads) sh.sub[i] = __ldcg(p.sub + row * p.nsub + i);
       __syncthreads();
-      filtered<BF16>(p, sh, row, r, m, -INFINITY, cut);
+      filtered<BF16, false>(p, sh, row, r, m, -INFINITY, cut, total);
       __syncthreads();
       continue;
     }
@@ -1058,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
 struct SamplePlan {
   int64_t rows;
   int nseg, nsub, nchunk;
-  size_t sub, sum, all, over, marked, st, hist, list_x, list_i, bytes;  // workspace offsets
+  size_t sub, sum, over, marked, st, hist, list_x, list_i, bytes;  // workspace offsets
 };
 SamplePlan plan_sample(int B, int M, int V) {
   SamplePlan s;
@@ -1074,7 +1092,6 @@ SamplePlan plan_sample(int B, int M, int V) {
   };
   s.sub = take(s.nsub * sizeof(float));
   s.sum = take(s.nchunk * sizeof(double));
-  s.all = take(s.nchunk * sizeof(double));
   s.over = take(s.nchunk * sizeof(double));
   s.marked = take(sizeof(int));  // (the rounding holds the count as well)
   s.st = take(sizeof(RowState));
@@ -1091,6 +1108,7 @@ tv_status launch_sample(const SampleParams& p, int sms, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(finish_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(border_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return record_cuda_error(e);
+  static_assert(4 * (sizeof(Shared) + 1024) <= 228 * 1024, "four blocks to an SM");
   auto blocks = [&](int64_t n) { return dim3((unsigned)std::min<int64_t>(n, 4 * (int64_t)sms)); };
   const int64_t units = p.rows * p.nchunk;
   tv_status r =
@@ -1154,7 +1172,6 @@ extern "C" tv_status tree_accept_sample(const void* logits, int logits_type, int
   p.logprob = logprob;
   p.sub = reinterpret_cast<float*>(ws + lp.sub);
   p.sum = reinterpret_cast<double*>(ws + lp.sum);
-  p.all = reinterpret_cast<double*>(ws + lp.all);
   p.over = reinterpret_cast<double*>(ws + lp.over);
   p.marked = reinterpret_cast<int*>(ws + lp.marked);
   p.st = reinterpret_cast<RowState*>(ws + lp.st);
