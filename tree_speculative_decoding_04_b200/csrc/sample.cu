@@ -29,9 +29,9 @@
 //   weigh   a histogram of the weights, to 2^-16, over 1/32-octave bins below the row's
 //           maximum; the block that brings a row's last segment finds the bins in
 //           which the border must lie (one or two)
-//   border  exact sums of the tokens that each chunk keeps for sure, and a list of the
-//           tokens in the border's bins; the last block of a row settles those and
-//           draws
+//   border  a list of the tokens down to the border's bins, or, if those are too many,
+//           of the tokens in the border's bins and exact sums of what each chunk keeps
+//           for sure; the last block of a row settles the list and draws
 //   walk    tree_accept's acceptance walk, on the drawn tokens
 // Weights are doubles (2^((l - m) log2e / T), relative error below 2^-48: a
 // token's share of a flat vocabulary is 2^-18, and a sum in fp32 would move the
@@ -78,7 +78,7 @@ struct SampleParams {
   float* sub;    // [rows][nsub] maxima of 128 tokens
   double* sum;   // [rows][nchunk] weight of a chunk relative to its maximum; after border: what it keeps for sure
   // rows whose top-p keeps many tokens
-  int* marked;         // [0] how many, [1 + i] their rows
+  int* marked;         // [0] how many, [1], [2] segments taken by weigh and border, [4 + i] their rows
   RowState* st;        // [rows]
   u64* hist;           // [rows][kBins] weights in units of 2^-18 of the bin's top
   double* over;        // [rows][nchunk] weight of a chunk's tokens above the border's bins
@@ -743,7 +743,7 @@ __device__ void finish_row(const SampleParams& p, Shared& sh, int64_t row) {
         st.m = m;
         st.scale = (float)fmin(32.0 * r.c, 3e38);
         p.st[row] = st;
-        p.marked[1 + atomicAdd(p.marked, 1)] = (int)row;
+        p.marked[4 + atomicAdd(p.marked, 1)] = (int)row;
       }
       return;
     }
@@ -797,13 +797,13 @@ __device__ __forceinline__ void unpack_chunk(const uint32_t (&raw)[BF16 ? 16 : 3
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 4) stream_kernel(const __grid_constant__ SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 3) stream_kernel(const __grid_constant__ SampleParams p) {
   __shared__ double tab[kTab * kTabCopies];
   const int tid = threadIdx.x, lane = tid & 31;
   fill_table(tab);
   pdl_wait_primary();
   pdl_launch_dependents();
-  if (blockIdx.x == 0 && tid == 0) p.marked[0] = 0;
+  if (blockIdx.x == 0 && tid < 4) p.marked[tid] = 0;
   __syncthreads();
   const int64_t units = p.rows * p.nchunk, step = (int64_t)gridDim.x * kWarps;
   int64_t unit = (int64_t)blockIdx.x * kWarps + (tid >> 5);
@@ -831,7 +831,12 @@ __global__ void __launch_bounds__(kThreads, 4) stream_kernel(const __grid_consta
       if (Weigher::fits(cm, r.c)) {
         const Weigher wt(cm, r.c);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) s += wt(x[e], tab);
+        for (int e0 = 0; e0 < 32; e0 += 8) {
+          double v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = wt(x[e0 + e], tab);
+          s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        }
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e) s += weight(clean(x[e]), cm, r.c, tab);
@@ -866,17 +871,41 @@ __device__ __forceinline__ bool last_segment(int* count, int nseg) {
   return last;
 }
 
+// The next segment of the marked rows for this block, requested one ahead.  (Taken
+// in turn: a block that has finished a row is late, and with a fixed share of the
+// segments it would be the last of its next rows too, and finish them all.)
+struct Segments {
+  int* taken;
+  int units, ahead;
+  __device__ __forceinline__ Segments(int* taken_, int units_) : taken(taken_), units(units_) {
+    ahead = threadIdx.x == 0 ? atomicAdd(taken, 1) : 0;
+  }
+  __device__ __forceinline__ int next() {  // -1: none left
+    __shared__ int unit;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      unit = ahead < units ? ahead : -1;
+      ahead = atomicAdd(taken, 1);
+    }
+    __syncthreads();
+    return unit;
+  }
+};
+
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const __grid_constant__ SampleParams p) {
   __shared__ uint32_t hist_s[kBins];  // (8192 tokens of at most 2^18 each stay below 2^32)
-  __shared__ u64 red[kWarps];
+  __shared__ u64 red[2 * kWarps];
+  __shared__ int too_many;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int64_t units = (int64_t)__ldcg(p.marked) * p.nseg;
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int64_t row = __ldcg(p.marked + 1 + unit / p.nseg);
-    const int chunk = (int)(unit % p.nseg) * kWarps + w;
+  const int units = __ldcg(p.marked) * p.nseg;
+  if (units == 0) return;
+  Segments segments(p.marked + 1, units);
+  for (int unit = segments.next(); unit >= 0; unit = segments.next()) {
+    const int64_t row = __ldcg(p.marked + 4 + unit / p.nseg);
+    const int chunk = unit % p.nseg * kWarps + w;
     for (int i = tid; i < kBins; i += kThreads) hist_s[i] = 0;
     __syncthreads();
     const float m = __ldcg(&p.st[row].m), scale = __ldcg(&p.st[row].scale);
@@ -898,17 +927,27 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const __grid_constan
     for (int i = tid; i < kBins; i += kThreads)
       if (hist_s[i]) atomicAdd(hist + i, (u64)hist_s[i]);
     if (!last_segment(&p.st[row].weighed, p.nseg)) continue;
-    // thread i sums bins 4 i .. 4 i + 3, in units of 2^-46
-    u64 v[4], s = 0;
+    // thread i sums bins 4 i .. 4 i + 3: weights in units of 2^-46, and tokens (in all
+    // bins but the last a token counts between 2^(18 - 1/32) and 2^18)
+    u64 v[4], s = 0, tokens = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[j] = (u64)((double)__ldcg(hist + 4 * tid + j) * (double)fast_exp2(28.f - (float)(4 * tid + j) / 32.f));
+      const u64 h = __ldcg(hist + 4 * tid + j);
+      v[j] = (u64)((double)h * (double)fast_exp2(28.f - (float)(4 * tid + j) / 32.f));
       s += v[j];
+      tokens += (h + 255999) / 256000;
     }
-    u64 incl = warp_scan(s);
-    if (lane == 31) red[w] = incl;
+    u64 incl = warp_scan(s), listed = warp_scan(tokens);
+    if (lane == 31) {
+      red[w] = incl;
+      red[kWarps + w] = listed;
+    }
+    if (tid == 0) too_many = 0;
     __syncthreads();
-    for (int i = 0; i < w; ++i) incl += red[i];
+    for (int i = 0; i < w; ++i) {
+      incl += red[i];
+      listed += red[kWarps + i];
+    }
     // Each weight is good to 2^-16: its 18 bits, the exponent's two fp32 roundings
     // (of up to 32: 2^-18) and the exponentials'.  The border lies behind the last
     // bin up to which the sum is surely too small, and not behind the first up to
@@ -920,15 +959,21 @@ __global__ void __launch_bounds__(kThreads, 4) weigh_kernel(const __grid_constan
     for (int j = 0; j < 4; ++j) {
       const double c0 = (double)cum, c1 = (double)(cum + v[j]);
       if ((c0 < first && c1 >= first) || (tid == kThreads - 1 && j == 3 && c1 < first)) p.st[row].bin0 = 4 * tid + j;
-      if ((c0 < last && c1 >= last) || (tid == kThreads - 1 && j == 3 && c1 < last)) p.st[row].bin1 = 4 * tid + j;
+      if ((c0 < last && c1 >= last) || (tid == kThreads - 1 && j == 3 && c1 < last)) {
+        p.st[row].bin1 = 4 * tid + j;
+        too_many = listed > kRowList || 4 * tid + j == kBins - 1;
+      }
       cum += v[j];
     }
+    __syncthreads();
+    // where all that may be kept fits the list, all of it is listed
+    if (tid == 0 && !too_many) p.st[row].bin0 = 0;
     __syncthreads();
   }
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_constant__ SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 3) border_kernel(const __grid_constant__ SampleParams p) {
   constexpr int kDrop = BF16 ? 16 : 0;
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
@@ -937,10 +982,12 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
   pdl_wait_primary();
   pdl_launch_dependents();
   __syncthreads();
-  const int64_t units = (int64_t)__ldcg(p.marked) * p.nseg;
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int64_t row = __ldcg(p.marked + 1 + unit / p.nseg);
-    const int chunk = (int)(unit % p.nseg) * kWarps + w;
+  const int units = __ldcg(p.marked) * p.nseg;
+  if (units == 0) return;
+  Segments segments(p.marked + 2, units);
+  for (int unit = segments.next(); unit >= 0; unit = segments.next()) {
+    const int64_t row = __ldcg(p.marked + 4 + unit / p.nseg);
+    const int chunk = unit % p.nseg * kWarps + w;
     const Rule r = rule_of(p, (int)(row / p.n));
     const double c = r.c;
     const float m = __ldcg(&p.st[row].m), scale = __ldcg(&p.st[row].scale), cut = min_p_cut(r, m);
@@ -955,16 +1002,27 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
       uint32_t listed = 0;  // bit e: x[e] goes to the list
       const Weigher wt(m, c);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const float xe = fmaxf(x[e], -INFINITY);
-        float frac;
-        const int bin = bin_of(xe, m, scale, frac);
-        if (__any_sync(0xffffffffu, bin < bin0)) {
-          const double v = bin < bin0 ? wt(xe, sh.tab) : 0.0;
-          over += v;
-          keep += over_cut(xe) ? v : 0.0;
+      for (int e0 = 0; e0 < 32; e0 += 8) {
+        // eight tokens at a time: their weights' chains of dependent steps overlap
+        uint32_t sure = 0;
+#pragma unroll
+        for (int e = e0; e < e0 + 8; ++e) {
+          x[e] = fmaxf(x[e], -INFINITY);
+          float frac;
+          const int bin = bin_of(x[e], m, scale, frac);
+          sure |= bin < bin0 ? 1u << e : 0u;
+          listed |= bin >= bin0 && bin <= bin1 && x[e] > -INFINITY ? 1u << e : 0u;
         }
-        listed |= bin >= bin0 && bin <= bin1 && xe > -INFINITY ? 1u << e : 0u;
+        if (!__any_sync(0xffffffffu, sure != 0)) continue;
+        double v[8];
+#pragma unroll
+        for (int e = e0; e < e0 + 8; ++e) v[e - e0] = wt(x[e], sh.tab);
+#pragma unroll
+        for (int e = e0; e < e0 + 8; ++e) {
+          const double s = (sure >> e) & 1u ? v[e - e0] : 0.0;
+          over += s;
+          keep += over_cut(x[e]) ? s : 0.0;
+        }
       }
       over = warp_sum(over);
       keep = warp_sum(keep);
@@ -1005,17 +1063,18 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
     const Source<BF16> src{p, sh, row, -INFINITY, true};
     auto key = [](float x, int) { return order_key(x) >> kDrop; };
     auto fixed = [&](float x) { return (u64)__double2ull_rn(weight(x, m, c, sh.tab) * unit_w); };
+    int tie_end = INT_MAX;
     if (settled) {
-      // the bins' tokens, in any order
+      // the bins' tokens, in any order, dealt to the warps in turn
       for (int i = tid; i < n; i += kThreads) {
-        sh.lval[i / kListCap][i % kListCap] = __ldcg(p.list_x + row * kRowList + i);
-        sh.lidx[i / kListCap][i % kListCap] = __ldcg(p.list_i + row * kRowList + i);
+        sh.lval[i % kWarps][i / kWarps] = __ldcg(p.list_x + row * kRowList + i);
+        sh.lidx[i % kWarps][i / kWarps] = __ldcg(p.list_i + row * kRowList + i);
       }
-      if (tid < kWarps) sh.len[tid] = max(0, min(kListCap, n - tid * kListCap));
-      uint32_t klo = 0xffffffffu, khi = 0;
+      if (tid < kWarps) sh.len[tid] = (n - tid + kWarps - 1) / kWarps;
       __syncthreads();
+      uint32_t klo = 0xffffffffu, khi = 0;
       for (int i = tid; i < n; i += kThreads) {
-        const uint32_t k = order_key(sh.lval[i / kListCap][i % kListCap]) >> kDrop;
+        const uint32_t k = order_key(sh.lval[i % kWarps][i / kWarps]) >> kDrop;
         klo = min(klo, k);
         khi = max(khi, k);
       }
@@ -1033,6 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
       if (settled) {
         const float xt = BF16 ? key_value(t << 16 | ((t & 0x8000u) ? 0u : 0xffffu)) : key_value(t);
         e = Border{t, tokens_below(above, fixed(xt), ties, want), ties};
+        if (e.c < e.ties) tie_end = tie_limit(src, sh, key, e.t, e.c);
       }
     }
     if (!settled) {
@@ -1044,7 +1104,6 @@ __global__ void __launch_bounds__(kThreads, 4) border_kernel(const __grid_consta
       __syncthreads();
       continue;
     }
-    const int tie_end = e.c < e.ties ? tie_limit(src, sh, key, e.t, e.c) : INT_MAX;
     auto in_bins = [&](float x, int i) {
       const uint32_t k = order_key(x) >> kDrop;
       return k > e.t || (k == e.t && i <= tie_end);
@@ -1108,15 +1167,17 @@ tv_status launch_sample(const SampleParams& p, int sms, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(finish_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(border_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return record_cuda_error(e);
+  // as many blocks as are resident at once (launch bounds; the finish's shared memory
+  // fits four times)
   static_assert(4 * (sizeof(Shared) + 1024) <= 228 * 1024, "four blocks to an SM");
-  auto blocks = [&](int64_t n) { return dim3((unsigned)std::min<int64_t>(n, 4 * (int64_t)sms)); };
+  auto blocks = [&](int64_t n, int per_sm) { return dim3((unsigned)std::min<int64_t>(n, per_sm * (int64_t)sms)); };
   const int64_t units = p.rows * p.nchunk;
   tv_status r =
-      launch(stream_kernel<BF16>, blocks((units + kWarps - 1) / kWarps), dim3(kThreads), 0, s, 1, true, p);
+      launch(stream_kernel<BF16>, blocks((units + kWarps - 1) / kWarps, 3), dim3(kThreads), 0, s, 1, true, p);
   if (r == TV_OK) r = launch(finish_kernel<BF16>, dim3((unsigned)p.rows), dim3(kThreads), smem, s, 1, true, p);
   if (r != TV_OK || !p.top_p) return r;
-  r = launch(weigh_kernel<BF16>, blocks(p.rows * p.nseg), dim3(kThreads), 0, s, 1, true, p);
-  if (r == TV_OK) r = launch(border_kernel<BF16>, blocks(p.rows * p.nseg), dim3(kThreads), smem, s, 1, true, p);
+  r = launch(weigh_kernel<BF16>, blocks(p.rows * p.nseg, 4), dim3(kThreads), 0, s, 1, true, p);
+  if (r == TV_OK) r = launch(border_kernel<BF16>, blocks(p.rows * p.nseg, 3), dim3(kThreads), smem, s, 1, true, p);
   return r;
 }
 
@@ -1145,6 +1206,7 @@ extern "C" tv_status tree_accept_sample(const void* logits, int logits_type, int
   if ((reinterpret_cast<uintptr_t>(logits) & (logits_type == TV_LOGITS_F32 ? 3u : 1u)) != 0) return TV_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)B * (M + 1);
   if (rows > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
+  if (rows * tv::plan_sample(1, 0, V).nseg > 0x3fffffff) return TV_ERR_UNSUPPORTED;  // segments are counted in 32 bits
   if (!workspace || !aligned16(workspace) || workspace_bytes < tree_accept_sample_workspace_size(B, M, V))
     return TV_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
