@@ -128,32 +128,60 @@ def _stream(stream):
 
 
 class _on:
-    """The device of the tensors as the current one for a call, and the call's
-    stream (the given one, else that device's current one) as its pointer.  All
-    tensors must live on that one GPU."""
+    """The device `dev` as the current one for a call, and the call's stream (the
+    given one, else that device's current one) as its pointer."""
 
     __slots__ = ("dev", "stream", "back")
 
-    def __init__(self, stream, *tensors):
-        self.dev, self.stream, self.back = tensors[0].get_device(), stream, -1
-        for t in tensors:
-            if t is not None and t.get_device() != self.dev:
-                raise TVError("tensors must live on one GPU")
+    def __init__(self, stream, dev):
+        self.dev, self.stream, self.back = dev, stream, -1
 
     def __enter__(self):
-        if self.dev < 0:
-            raise TVError("tensor must live on the GPU")
-        if torch.cuda.current_device() != self.dev:
-            self.back = torch.cuda.current_device()
+        current = torch._C._cuda_getDevice()
+        if current != self.dev:
+            self.back = current
             torch.cuda.set_device(self.dev)
         if self.stream is None:
-            return ctypes.c_void_p(torch.cuda.current_stream(self.dev).cuda_stream)
-        return ctypes.c_void_p(self.stream.cuda_stream)
+            return torch._C._cuda_getCurrentRawStream(self.dev)
+        return self.stream.cuda_stream
 
     def __exit__(self, *exc):
         if self.back >= 0:
             torch.cuda.set_device(self.back)
         return False
+
+
+def _arg(t, dtype, shape, name, dev, rows=False):
+    """The address of a checked argument: dtype, shape, the call's GPU, contiguous
+    (rows: its strides are checked by _row_stride)."""
+    if t.dtype is not dtype:
+        raise TVError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise TVError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise TVError("tensors must live on one GPU" if t.is_cuda else "tensor must live on the GPU")
+    if not rows and not t.is_contiguous():
+        raise TVError("tensor must be contiguous")
+    return t.data_ptr()
+
+
+def _scratch(t, dev):
+    """(address, bytes) of a workspace tensor, or (None, 0)."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev:
+        raise TVError("tensors must live on one GPU" if t.is_cuda else "tensor must live on the GPU")
+    if not t.is_contiguous():
+        raise TVError("tensor must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _gpu_of(t) -> int:
+    """The GPU of a call's first tensor; the others must live there too."""
+    dev = t.get_device()
+    if dev < 0:
+        raise TVError("tensor must live on the GPU")
+    return dev
 
 
 def _row_stride(t: torch.Tensor, width: int, name: str) -> int:
@@ -172,12 +200,6 @@ def _row_stride(t: torch.Tensor, width: int, name: str) -> int:
     if row < width or (B > 1 and n > 1 and t.stride(0) != n * row):
         raise TVError(f"{name}: rows must be evenly spaced")
     return row
-
-
-def _ptr_rows(t: torch.Tensor):
-    if not t.is_cuda:
-        raise TVError("tensor must live on the GPU")
-    return ctypes.c_void_p(t.data_ptr())
 
 
 def _need(t: torch.Tensor, dtype, shape, name):
@@ -314,27 +336,22 @@ def tree_attention_scored(q, k, v, kv_start, kv_len, anc_mask, depth, status, ou
     B, n, Hq, D = q.shape
     Hkv, S_cap = k.shape[1], k.shape[2]
     NS = k.shape[0] if slot is not None else B
-    _need(q, torch.bfloat16, (B, n, Hq, D), "q")
-    _need(k, torch.bfloat16, (NS, Hkv, S_cap, D), "k")
-    _need(v, torch.bfloat16, (NS, Hkv, S_cap, D), "v")
-    _need(kv_start, torch.int32, (NS,), "kv_start")
-    _need(kv_len, torch.int32, (NS,), "kv_len")
-    _need(anc_mask, torch.int32, (B, n, (n + 31) // 32), "anc_mask")
-    _need(depth, torch.int32, (B, n), "depth")
-    _need(status, torch.int32, (B,), "status")
-    _need(out, torch.bfloat16, (B, n, Hq, D), "out")
-    if slot is not None:
-        _need(slot, torch.int32, (B,), "slot")
-    if alibi_slopes is not None:
-        _need(alibi_slopes, torch.float32, (Hq,), "alibi_slopes")
+    bf, i32 = torch.bfloat16, torch.int32
+    # (shapes and types first: they are wrong on any device)
+    dev = q.get_device()
+    a_q, a_k, a_v = (_arg(q, bf, (B, n, Hq, D), "q", dev), _arg(k, bf, (NS, Hkv, S_cap, D), "k", dev),
+                     _arg(v, bf, (NS, Hkv, S_cap, D), "v", dev))
+    a_ks, a_kl = _arg(kv_start, i32, (NS,), "kv_start", dev), _arg(kv_len, i32, (NS,), "kv_len", dev)
+    a_anc, a_dep = _arg(anc_mask, i32, (B, n, (n + 31) // 32), "anc_mask", dev), _arg(depth, i32, (B, n), "depth", dev)
+    a_st, a_out = _arg(status, i32, (B,), "status", dev), _arg(out, bf, (B, n, Hq, D), "out", dev)
+    a_slot = None if slot is None else _arg(slot, i32, (B,), "slot", dev)
+    a_slopes = None if alibi_slopes is None else _arg(alibi_slopes, torch.float32, (Hq,), "alibi_slopes", dev)
+    a_ws, ws_bytes = _scratch(workspace, dev)
     if scale is None:
         scale = D ** -0.5
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on(stream, q, k, v, kv_start, kv_len, anc_mask, depth, status, out, workspace, alibi_slopes, slot) as s:
-        rc = load().tree_attention_scored(_ptr(q), _ptr(k), _ptr(v), S_cap, _ptr(kv_start), _ptr(kv_len),
-                                          _ptr(anc_mask), _ptr(depth), _ptr(status), B, n - 1, Hq, Hkv, D,
-                                          float(scale), float(softcap), int(window), _ptr(alibi_slopes), _ptr(out),
-                                          _ptr(workspace), ws_bytes, _ptr(slot), NS, s)
+    with _on(stream, _gpu_of(q)) as s:
+        rc = load().tree_attention_scored(a_q, a_k, a_v, S_cap, a_ks, a_kl, a_anc, a_dep, a_st, B, n - 1, Hq, Hkv, D,
+                                          float(scale), float(softcap), int(window), a_slopes, a_out, a_ws, ws_bytes, a_slot, NS, s)
     _check(rc, "tree_attention_scored")
 
 
@@ -358,30 +375,26 @@ def tree_accept_sample(logits, uniform, temperature, draft, parent, depth, anc_m
     B, n, V = logits.shape
     if logits.dtype not in (torch.float32, torch.bfloat16):
         raise TVError(f"logits: dtype {logits.dtype}, expected torch.float32 or torch.bfloat16")
+    i32, f32, md = torch.int32, torch.float32, int(max_depth)
+    dev = logits.get_device()
     stride = _row_stride(logits, V, "logits")
-    for t, name in ((uniform, "uniform"), (logprob, "logprob")):
-        if t is not None or name == "uniform":
-            _need(t, torch.float32, (B, n), name)
-    for t, name in ((draft, "draft"), (parent, "parent"), (depth, "depth"), (token, "token")):
-        _need(t, torch.int32, (B, n), name)
-    _need(temperature, torch.float32, (B,), "temperature")
-    if top_k is not None:
-        _need(top_k, torch.int32, (B,), "top_k")
-    for t, name in ((top_p, "top_p"), (min_p, "min_p")):
-        if t is not None:
-            _need(t, torch.float32, (B,), name)
-    _need(anc_mask, torch.int32, (B, n, (n + 31) // 32), "anc_mask")
-    _need(status, torch.int32, (B,), "status")
-    _need(accept_len, torch.int32, (B,), "accept_len")
-    _need(path, torch.int32, (B, int(max_depth) + 1), "path")
-    _need(bonus, torch.int32, (B,), "bonus")
-    with _on(stream, logits, uniform, temperature, draft, parent, depth, anc_mask, status, token, accept_len, path,
-             bonus, workspace, top_k, top_p, min_p, logprob) as s:
-        rc = load().tree_accept_sample(_ptr_rows(logits), int(logits.dtype == torch.bfloat16), stride, _ptr(uniform),
-                                       _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(draft),
-                                       _ptr(parent), _ptr(depth), _ptr(anc_mask), _ptr(status), B, n - 1, V,
-                                       int(max_depth), _ptr(token), _ptr(logprob), _ptr(accept_len), _ptr(path),
-                                       _ptr(bonus), _ptr(workspace), workspace.numel() * workspace.element_size(), s)
+    per_node, per_row = (B, n), (B,)
+    a_u = _arg(uniform, f32, per_node, "uniform", dev)
+    a_T = _arg(temperature, f32, per_row, "temperature", dev)
+    a_k = None if top_k is None else _arg(top_k, i32, per_row, "top_k", dev)
+    a_p = None if top_p is None else _arg(top_p, f32, per_row, "top_p", dev)
+    a_m = None if min_p is None else _arg(min_p, f32, per_row, "min_p", dev)
+    a_lp = None if logprob is None else _arg(logprob, f32, per_node, "logprob", dev)
+    a_draft, a_par = _arg(draft, i32, per_node, "draft", dev), _arg(parent, i32, per_node, "parent", dev)
+    a_dep, a_tok = _arg(depth, i32, per_node, "depth", dev), _arg(token, i32, per_node, "token", dev)
+    a_anc, a_st = _arg(anc_mask, i32, (B, n, (n + 31) // 32), "anc_mask", dev), _arg(status, i32, per_row, "status", dev)
+    a_al, a_path = _arg(accept_len, i32, per_row, "accept_len", dev), _arg(path, i32, (B, md + 1), "path", dev)
+    a_bonus = _arg(bonus, i32, per_row, "bonus", dev)
+    a_ws, ws_bytes = _scratch(workspace, dev)
+    with _on(stream, _gpu_of(logits)) as s:
+        rc = load().tree_accept_sample(logits.data_ptr(), int(logits.dtype is torch.bfloat16), stride, a_u, a_T, a_k,
+                                       a_p, a_m, a_draft, a_par, a_dep, a_anc, a_st, B, n - 1, V, md, a_tok, a_lp, a_al,
+                                       a_path, a_bonus, a_ws, ws_bytes, s)
     _check(rc, "tree_accept_sample")
 
 
@@ -399,24 +412,21 @@ def tree_qk_norm_rope(qkv, q_weight, k_weight, q_out, k, v, kv_start, kv_len, de
     Hkv, S_cap = k.shape[1], k.shape[2]
     NS = k.shape[0] if slot is not None else B
     heads = Hq + 2 * Hkv
-    _need(qkv, torch.bfloat16, (B, n, heads, D), "qkv")
+    bf, i32 = torch.bfloat16, torch.int32
+    dev = q_out.get_device()
+    a_qkv = _arg(qkv, bf, (B, n, heads, D), "qkv", dev, rows=True)
     stride = _row_stride(qkv, heads * D, "qkv")
-    _need(q_out, torch.bfloat16, (B, n, Hq, D), "q_out")
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _need(t, torch.bfloat16, (D,), name)
-    _need(k, torch.bfloat16, (NS, Hkv, S_cap, D), "k")
-    _need(v, torch.bfloat16, (NS, Hkv, S_cap, D), "v")
-    _need(kv_start, torch.int32, (NS,), "kv_start")
-    _need(kv_len, torch.int32, (NS,), "kv_len")
-    _need(depth, torch.int32, (B, n), "depth")
-    if slot is not None:
-        _need(slot, torch.int32, (B,), "slot")
-    with _on(stream, q_out, qkv, q_weight, k_weight, k, v, kv_start, kv_len, depth, slot) as s:
-        rc = load().tree_qk_norm_rope(_ptr_rows(qkv), stride, _ptr(q_weight), _ptr(k_weight), float(weight_offset),
-                                      float(eps), _ptr(q_out), _ptr(k), _ptr(v), S_cap, _ptr(kv_start), _ptr(kv_len),
-                                      _ptr(depth), B, n - 1, Hq, Hkv, D, D if rotary_dim is None else int(rotary_dim),
-                                      float(rope_theta), _ptr(slot), NS, s)
+    a_qo = _arg(q_out, bf, (B, n, Hq, D), "q_out", dev)
+    a_wq = None if q_weight is None else _arg(q_weight, bf, (D,), "q_weight", dev)
+    a_wk = None if k_weight is None else _arg(k_weight, bf, (D,), "k_weight", dev)
+    a_k, a_v = _arg(k, bf, (NS, Hkv, S_cap, D), "k", dev), _arg(v, bf, (NS, Hkv, S_cap, D), "v", dev)
+    a_ks, a_kl = _arg(kv_start, i32, (NS,), "kv_start", dev), _arg(kv_len, i32, (NS,), "kv_len", dev)
+    a_dep = _arg(depth, i32, (B, n), "depth", dev)
+    a_slot = None if slot is None else _arg(slot, i32, (B,), "slot", dev)
+    with _on(stream, _gpu_of(q_out)) as s:
+        rc = load().tree_qk_norm_rope(a_qkv, stride, a_wq, a_wk, float(weight_offset), float(eps), a_qo, a_k, a_v, S_cap, a_ks, a_kl,
+                                      a_dep, B, n - 1, Hq, Hkv, D, D if rotary_dim is None else int(rotary_dim),
+                                      float(rope_theta), a_slot, NS, s)
     _check(rc, "tree_qk_norm_rope")
 
 

@@ -1011,11 +1011,8 @@ struct ScoredPlan {
 };
 
 tv_status plan_scored(int B, int M, int Hq, int Hkv, int D, int64_t S_cap, int window, ScoredPlan& lp) {
-  int dev = 0;
-  lp.sms = 148;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&lp.sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return record_cuda_error(e);
+  const tv_status r = current_sms(lp.sms);
+  if (r != TV_OK) return r;
   const int rows = (Hq / Hkv) * (M + 1);
   lp.nqt = (rows + kQRows - 1) / kQRows;
   lp.npairs = (lp.nqt + 1) / 2;
@@ -1044,9 +1041,9 @@ tv_status launch_scored(int mode, const CUtensorMap& tmk, const CUtensorMap& tmv
               : mode == kBias    ? scored_kernel<D, kBias>
                                  : scored_kernel<D, kCapBias>;
   const size_t smem = 2 * (D / 64) * kQHalf + kRingBytes + sizeof(Shared);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return record_cuda_error(e);
-  tv_status r = launch(kern, dim3((unsigned)lp.grid), dim3(kThreads), smem, s, 1, true, tmk, tmv, p);
+  tv_status r = allow_shared(reinterpret_cast<const void*>(kern), (int)smem);
+  if (r != TV_OK) return r;
+  r = launch(kern, dim3((unsigned)lp.grid), dim3(kThreads), smem, s, 1, true, tmk, tmv, p);
   if (r != TV_OK || !lp.split) return r;
   // about four blocks an SM (at most 16 have work per unit): most find a sequence in one range and leave
   const int units = p.B * p.Hkv * p.nqt;

@@ -1,6 +1,9 @@
 // capi.cu -- status strings, version and the per-thread record of the last
 // CUDA error for the tree verification C ABI.
 #include <atomic>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "tv_common.cuh"
 
@@ -19,6 +22,41 @@ tv_status record_cuda_error(cudaError_t e) {
   g_last_cuda_error = static_cast<int>(e);
   (void)cudaGetLastError();  // clear the sticky-free launch error so later calls start clean
   return TV_ERR_CUDA;
+}
+
+namespace {
+std::mutex g_device_mutex;
+std::map<int, int> g_sms;                                   // by device
+std::map<std::pair<int, const void*>, int> g_shared_bytes;  // by device and kernel
+}  // namespace
+
+tv_status current_sms(int& sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  std::lock_guard<std::mutex> lock(g_device_mutex);
+  const auto it = g_sms.find(dev);
+  if (it != g_sms.end()) {
+    sms = it->second;
+    return TV_OK;
+  }
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  g_sms[dev] = sms;
+  return TV_OK;
+}
+
+tv_status allow_shared(const void* kernel, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  std::lock_guard<std::mutex> lock(g_device_mutex);
+  int& have = g_shared_bytes[{dev, kernel}];
+  if (have >= bytes) return TV_OK;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  have = bytes;
+  return TV_OK;
 }
 
 }  // namespace tv

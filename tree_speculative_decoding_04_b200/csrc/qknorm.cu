@@ -179,7 +179,18 @@ extern "C" tv_status tree_qk_norm_rope(const uint16_t* qkv, int64_t qkv_stride, 
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.R = rotary_dim;
-  rope_freqs(rotary_dim > 0 ? (double)rope_theta : 2.0, std::max(rotary_dim, 2), p.rope);
+  // (a program's layers share their base: the last table is kept per thread)
+  thread_local struct {
+    float theta = 0.f;
+    int dim = 0;
+    RopeFreqs f;
+  } last;
+  if (rotary_dim > 0 && (last.theta != rope_theta || last.dim != rotary_dim)) {
+    rope_freqs((double)rope_theta, rotary_dim, last.f);
+    last.theta = rope_theta;
+    last.dim = rotary_dim;
+  }
+  p.rope = last.f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   auto kern = D == 64 ? qk_norm_rope_kernel<64> : qk_norm_rope_kernel<128>;
   return launch(kern, dim3((unsigned)rows), dim3(256), 0, s, 1, true, p);

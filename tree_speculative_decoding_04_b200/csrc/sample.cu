@@ -1164,16 +1164,15 @@ SamplePlan plan_sample(int B, int M, int V) {
 template <bool BF16>
 tv_status launch_sample(const SampleParams& p, int sms, cudaStream_t s) {
   const int smem = (int)sizeof(Shared);
-  cudaError_t e = cudaFuncSetAttribute(finish_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(border_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return record_cuda_error(e);
+  tv_status r = allow_shared(reinterpret_cast<const void*>(finish_kernel<BF16>), smem);
+  if (r == TV_OK && p.top_p) r = allow_shared(reinterpret_cast<const void*>(border_kernel<BF16>), smem);
+  if (r != TV_OK) return r;
   // as many blocks as are resident at once (launch bounds; the finish's shared memory
   // fits four times)
   static_assert(4 * (sizeof(Shared) + 1024) <= 228 * 1024, "four blocks to an SM");
   auto blocks = [&](int64_t n, int per_sm) { return dim3((unsigned)std::min<int64_t>(n, per_sm * (int64_t)sms)); };
   const int64_t units = p.rows * p.nchunk;
-  tv_status r =
-      launch(stream_kernel<BF16>, blocks((units + kWarps - 1) / kWarps, 3), dim3(kThreads), 0, s, 1, true, p);
+  r = launch(stream_kernel<BF16>, blocks((units + kWarps - 1) / kWarps, 3), dim3(kThreads), 0, s, 1, true, p);
   if (r == TV_OK) r = launch(finish_kernel<BF16>, dim3((unsigned)p.rows), dim3(kThreads), smem, s, 1, true, p);
   if (r != TV_OK || !p.top_p) return r;
   r = launch(weigh_kernel<BF16>, blocks(p.rows * p.nseg, 4), dim3(kThreads), 0, s, 1, true, p);
@@ -1210,10 +1209,9 @@ extern "C" tv_status tree_accept_sample(const void* logits, int logits_type, int
   if (!workspace || !aligned16(workspace) || workspace_bytes < tree_accept_sample_workspace_size(B, M, V))
     return TV_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int dev = 0, sms = 148;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return record_cuda_error(e);
+  int sms = 0;
+  tv_status r = current_sms(sms);
+  if (r != TV_OK) return r;
   const SamplePlan lp = plan_sample(B, M, V);
   char* ws = static_cast<char*>(workspace);
   SampleParams p;
@@ -1241,8 +1239,7 @@ extern "C" tv_status tree_accept_sample(const void* logits, int logits_type, int
   p.list_x = reinterpret_cast<float*>(ws + lp.list_x);
   p.list_i = reinterpret_cast<int*>(ws + lp.list_i);
   p.shift = V <= (1 << 17) ? 46 : 45;
-  const tv_status r =
-      logits_type == TV_LOGITS_F32 ? launch_sample<false>(p, sms, s) : launch_sample<true>(p, sms, s);
+  r = logits_type == TV_LOGITS_F32 ? launch_sample<false>(p, sms, s) : launch_sample<true>(p, sms, s);
   if (r != TV_OK) return r;
   return launch_accept_walk(token, draft, parent, depth, anc_mask, status, B, M, max_depth, accept_len, path, bonus,
                             s);

@@ -284,6 +284,12 @@ tv_status launch_accept_walk(const int32_t* argmax, const int32_t* draft, const 
                              const int32_t* depth, const uint32_t* anc_mask, int32_t* status, int B, int M,
                              int max_depth, int32_t* accept_len, int32_t* path, int32_t* bonus, cudaStream_t s);
 
+// Multiprocessors of the current device (queried once per device and process).
+tv_status current_sms(int& sms);
+// Lets the current device launch `kernel` with up to `bytes` of dynamic shared memory
+// (asked of the runtime once per device and kernel).
+tv_status allow_shared(const void* kernel, int bytes);
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Launch with optional cluster dims and programmatic-dependent-launch attribute.
