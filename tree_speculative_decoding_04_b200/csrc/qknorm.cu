@@ -19,6 +19,8 @@
 namespace tv {
 namespace {
 
+constexpr int kNormThreads = 320;
+
 struct QkNormParams {
   const uint16_t* qkv;
   int64_t stride;  // elements between projection rows
@@ -53,79 +55,93 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 }
 
 // One CTA per projection row.  D / 16 lanes share a head; each holds two 16-byte
-// chunks of it: the two ends of eight rotated pairs, or two chunks past R.
+// chunks of it: the two ends of eight rotated pairs, or two chunks past R.  A warp
+// takes 512 / D heads at a time and requests the next ones before it works on
+// these, the first before the angles and weights are laid out in shared memory.
 template <int D>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const __grid_constant__ QkNormParams p) {
-  constexpr int kLanes = D / 16;
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  __shared__ float cs[D / 2], sn[D / 2];
+__global__ void __launch_bounds__(kNormThreads, 4) qk_norm_rope_kernel(const __grid_constant__ QkNormParams p) {
+  constexpr int kLanes = D / 16, kHeads = 32 / kLanes;
+  __shared__ __align__(16) float cs[D / 2], sn[D / 2], weight[2][D];
   const int n = p.M + 1;
   const int64_t row = blockIdx.x;
-  const int b = (int)(row / n), r = (int)(row % n);
-  const int sl = cache_slot(p.slot, b, p.n_slots);
-  if (sl < 0) return;
-  const int32_t ks = p.kv_start[sl], kl = p.kv_len[sl];
-  if (!geometry_ok(ks, kl, p.M, p.S_cap)) return;
+  const int b = (int)(row / n), r = (int)(row - (int64_t)b * n);
   const int half = p.R / 2;
-  if ((int)threadIdx.x < half)
-    rope_cos_sin(kl + p.depth[row], p.rope.f[threadIdx.x], cs[threadIdx.x], sn[threadIdx.x]);
-  __syncthreads();
-
-  const int c = threadIdx.x % kLanes;
+  const int lane = threadIdx.x & 31, step = (blockDim.x >> 5) * kHeads;
+  const int c = lane % kLanes;
   const bool rot = c < p.R / 16;
   const int c0 = rot ? c : 2 * c;          // past R: chunks R/8 + 2 (c - R/16) and the next
   const int c1 = rot ? c + p.R / 16 : 2 * c + 1;
   const int heads = p.Hq + 2 * p.Hkv;
-  for (int h = threadIdx.x / kLanes; h < (heads + 7) / 8 * 8; h += blockDim.x / kLanes) {
-    const bool in = h < heads;  // whole warps stay together for the shuffles
-    const uint4* src = reinterpret_cast<const uint4*>(p.qkv + row * p.stride + (int64_t)h * D);
-    const uint4 a = in ? src[c0] : make_uint4(0, 0, 0, 0);
-    const uint4 e = in ? src[c1] : make_uint4(0, 0, 0, 0);
+  const uint4* src = reinterpret_cast<const uint4*>(p.qkv + row * p.stride);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  int h = (threadIdx.x >> 5) * kHeads + lane / kLanes;
+  uint4 a = h < heads ? __ldg(src + h * (D / 8) + c0) : zero;
+  uint4 e = h < heads ? __ldg(src + h * (D / 8) + c1) : zero;
+  for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {  // (no weight: a scale of one)
+    const uint16_t* w = i < D ? p.q_weight : p.k_weight;
+    weight[i / D][i % D] = w ? p.offset + __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[i % D]) : 1.f;
+  }
+  const int depth = p.depth[row];
+  const int sl = cache_slot(p.slot, b, p.n_slots);
+  if (sl < 0) return;
+  const int32_t ks = p.kv_start[sl], kl = p.kv_len[sl];
+  if (!geometry_ok(ks, kl, p.M, p.S_cap)) return;
+  for (int i = threadIdx.x; i < half; i += blockDim.x) rope_cos_sin(kl + depth, p.rope.f[i], cs[i], sn[i]);
+  __syncthreads();
+  const int64_t col = ((int64_t)sl * p.Hkv * p.S_cap + ks + kl + r) * D;  // of the slot's first cache head
+  for (int first = 0; first < heads; first += step, h += step) {  // whole warps stay together for the shuffles
     float x[8], y[8];
     unpack8(a, x);
     unpack8(e, y);
+    const uint4 a0 = a, e0 = e;
+    if (h + step < heads) {
+      a = __ldg(src + (h + step) * (D / 8) + c0);
+      e = __ldg(src + (h + step) * (D / 8) + c1);
+    }
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss += x[i] * x[i] + y[i] * y[i];
 #pragma unroll
     for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    if (!in) continue;
+    if (h >= heads) continue;
     if (h >= p.Hq + p.Hkv) {
-      uint4* dst = reinterpret_cast<uint4*>(p.v + (((int64_t)sl * p.Hkv + h - p.Hq - p.Hkv) * p.S_cap + ks + kl + r) * D);
-      dst[c0] = a;
-      dst[c1] = e;
+      uint4* dst = reinterpret_cast<uint4*>(p.v + col + (int64_t)(h - p.Hq - p.Hkv) * p.S_cap * D);
+      dst[c0] = a0;
+      dst[c1] = e0;
       continue;
     }
     const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-    const uint16_t* wt = h < p.Hq ? p.q_weight : p.k_weight;
-    float w0[8], w1[8];
+    const bool is_q = h < p.Hq;
+    const float4* w0 = reinterpret_cast<const float4*>(weight[is_q ? 0 : 1]) + 2 * c0;
+    const float4* w1 = reinterpret_cast<const float4*>(weight[is_q ? 0 : 1]) + 2 * c1;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w0[i] = w1[i] = 1.f;
-    if (wt) {
-      unpack8(reinterpret_cast<const uint4*>(wt)[c0], w0);
-      unpack8(reinterpret_cast<const uint4*>(wt)[c1], w1);
+    for (int i = 0; i < 8; i += 4) {
+      const float4 u = w0[i / 4], v = w1[i / 4];
+      const float wu[4] = {u.x, u.y, u.z, u.w}, wv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        w0[i] += p.offset;
-        w1[i] += p.offset;
+      for (int j = 0; j < 4; ++j) {
+        x[i + j] *= inv * wu[j];
+        y[i + j] *= inv * wv[j];
       }
     }
+    if (rot) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float s = x[i] * inv * w0[i], t = y[i] * inv * w1[i];
-      if (rot) {
-        const float co = cs[8 * c + i], si = sn[8 * c + i];
-        const float s2 = fmaf(s, co, -t * si);
-        t = fmaf(t, co, s * si);
-        s = s2;
+      for (int i = 0; i < 8; i += 4) {
+        const float4 u = reinterpret_cast<const float4*>(cs)[2 * c + i / 4];
+        const float4 v = reinterpret_cast<const float4*>(sn)[2 * c + i / 4];
+        const float co[4] = {u.x, u.y, u.z, u.w}, si[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float s = x[i + j], t = y[i + j];
+          x[i + j] = fmaf(s, co[j], -t * si[j]);
+          y[i + j] = fmaf(t, co[j], s * si[j]);
+        }
       }
-      x[i] = s;
-      y[i] = t;
     }
-    uint4* dst = h < p.Hq
-                     ? reinterpret_cast<uint4*>(p.q_out + (row * p.Hq + h) * D)
-                     : reinterpret_cast<uint4*>(p.k + (((int64_t)sl * p.Hkv + h - p.Hq) * p.S_cap + ks + kl + r) * D);
+    uint4* dst = is_q ? reinterpret_cast<uint4*>(p.q_out + (row * p.Hq + h) * D)
+                      : reinterpret_cast<uint4*>(p.k + col + (int64_t)(h - p.Hq) * p.S_cap * D);
     dst[c0] = pack8(x);
     dst[c1] = pack8(y);
   }
@@ -193,5 +209,8 @@ extern "C" tv_status tree_qk_norm_rope(const uint16_t* qkv, int64_t qkv_stride, 
   p.rope = last.f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   auto kern = D == 64 ? qk_norm_rope_kernel<64> : qk_norm_rope_kernel<128>;
-  return launch(kern, dim3((unsigned)rows), dim3(256), 0, s, 1, true, p);
+  // a warp per group of heads, up to kNormThreads: two or three groups each for wide rows
+  const int per_warp = 512 / D, groups = (Hq + 2 * Hkv + per_warp - 1) / per_warp;
+  const int warps = std::min(kNormThreads / 32, groups);
+  return launch(kern, dim3((unsigned)rows), dim3(32 * warps), 0, s, 1, true, p);
 }
