@@ -227,6 +227,9 @@ tv_status tree_attention_noalloc(const uint16_t* q, const uint16_t* k, const uin
  * Contract: the K/V rows that some query row of the sequence may read hold
  * finite values; prefix columns before the root's window are not used, whatever
  * they hold.
+ * TV_ERR_UNSUPPORTED: B > 4096, (Hq / Hkv) * (M + 1) >= 2^21, scale > 10^4 softcap.
+ * The softmax weights are rounded to bf16 before their product with V; scores,
+ * sums and the merge of split key ranges are fp32.
  */
 size_t tree_attention_scored_workspace_size(int B, int M, int Hq, int Hkv, int D, int64_t S_cap, int window);
 
@@ -323,7 +326,7 @@ tv_status tree_accept_lm_head(const uint16_t* hidden, const uint16_t* w_lm, cons
  *              status unchanged)
  *   logprob    fp32 [B][M+1] out, may be NULL: log of the drawn token's
  *              probability among the kept tokens (-inf where token = -1)
- *   1 <= V <= 262144 (TV_ERR_UNSUPPORTED above).
+ *   1 <= V <= 262144; B (M + 1) ceil(V / 8192) < 2^30 (TV_ERR_UNSUPPORTED above)
  *   workspace  device scratch of tree_accept_sample_workspace_size(...) bytes, 16-byte
  *              aligned: no initialisation, dead after the call, not shared by
  *              calls (or captured graphs) that overlap on the device

@@ -382,3 +382,196 @@ def test_accept_sample_many_rows(orc):
     T = 0.3 + rng.random(12)
     _check_sample(orc, x, u, T, par, draft, 9, rng.integers(0, 90, 12), 0.5 + 0.6 * rng.random(12),
                   0.2 * rng.random(12) - 0.1)
+
+
+# ----------------------------------------------------------------------------- together
+
+def _teacher(seed, B=3, M=9, Hq=8, Hkv=2, D=64, V=3000, L=2, prefix=(150, 40, 97), window=(0, 60)):
+    """A TreeVerifier of a teacher with normalised heads, capped scores, a local layer and sampled decoding, its
+    packed projections and weights."""
+    from tree_speculative_decoding_04_b200.verifier import TreeVerifier
+
+    rng = np.random.default_rng(seed)
+    g = W.torch_generator(seed, dev())
+    S_cap = max(prefix) + 3 * (M + 1) + 8
+    ver = TreeVerifier(B, M, Hq, Hkv, D, V, L, S_cap, max_depth=6, softcap=30.0, window=window, sampling=True)
+    for layer in range(L):
+        ver.k[layer].copy_(W.randn_bf16((B, Hkv, S_cap, D), g, dev()))
+        ver.v[layer].copy_(W.randn_bf16((B, Hkv, S_cap, D), g, dev()))
+    ver.kv_len.copy_(i32(np.array(prefix[:B])))
+    ver.temperature.copy_(torch.tensor([0.8, 0.0, 1.2][:B]))
+    ver.top_k.copy_(i32([0, 0, 50][:B]))
+    ver.top_p.copy_(torch.tensor([0.9, 1.0, 0.95][:B]))
+    wq, wk = (W.randn_bf16((D,), g, dev()) * 0.2 for _ in range(2))
+    qkv = [W.randn_bf16((B, M + 1, Hq + 2 * Hkv, D), g, dev()) for _ in range(L)]
+    return ver, qkv, wq, wk, rng
+
+
+def _new_inputs(ver, qkv, rng, g):
+    par = parents(ver.B, ver.M, 6, rng)
+    ver.parent.copy_(i32(par))
+    logits = torch.as_tensor(rng.normal(0, 2, ver.logits.shape).astype(np.float32))
+    ver.logits.copy_(logits)
+    top = logits.argmax(-1).numpy()
+    draft = np.take_along_axis(top, par, 1).astype(np.int32)
+    draft[:, ::4] = rng.integers(0, ver.V, draft[:, ::4].shape)
+    ver.draft.copy_(i32(draft))
+    ver.uniform.copy_(torch.as_tensor(rng.random((ver.B, ver.n)).astype(np.float32)))
+    for t in qkv:
+        t.copy_(W.randn_bf16(tuple(t.shape), g, dev()))
+    return par, draft
+
+
+def _step(ver, qkv, wq, wk):
+    ver.build_mask()
+    for layer in range(ver.L):
+        ver.norm_rope(layer, qkv[layer], wq, wk, eps=1e-6, weight_offset=1.0, rope_theta=1e4, rotary_dim=ver.D // 2)
+        ver.attention(layer)
+    ver.accept()
+    ver.commit()
+
+
+def test_a_step_of_the_three_operators(orc):
+    """norm_rope -> attention of a capped and of a local layer -> sampled acceptance -> commit, each against its
+    reference on what the one before it left; two steps, so that the second works on the committed cache."""
+    ver, qkv, wq, wk, rng = _teacher(1)
+    g = W.torch_generator(2, dev())
+    for _ in range(2):
+        par, draft = _new_inputs(ver, qkv, rng, g)
+        ks, kl = ver.kv_start.cpu().numpy(), ver.kv_len.cpu().numpy()
+        before = [(k.clone(), v.clone()) for k, v in zip(ver.k, ver.v)]
+        ver.build_mask()
+        for layer in range(ver.L):
+            ver.norm_rope(layer, qkv[layer], wq, wk, eps=1e-6, weight_offset=1.0, rope_theta=1e4, rotary_dim=32)
+            ver.attention(layer)
+            rq, rk, rv, qmag, kmag = orc.tree_qk_norm_rope(
+                W.bf16_bits(qkv[layer]), W.bf16_bits(wq), W.bf16_bits(wk), 1.0, 1e-6, W.bf16_bits(before[layer][0]),
+                W.bf16_bits(before[layer][1]), ks, kl, ver.depth.cpu().numpy(), ver.Hq, ver.Hkv, 32, 1e4)
+            assert (np.abs(ver.q[layer].double().cpu().numpy() - rq) <= rope_tolerance(rq, qmag)).all()
+            gk = ver.k[layer].double().cpu().numpy()
+            assert (np.abs(gk - rk) <= np.where(kmag > 0, rope_tolerance(rk, kmag), 0.0)).all()
+            np.testing.assert_array_equal(ver.v[layer].double().cpu().numpy(), rv)
+            _check_attn(ver.out[layer], ver.q[layer], ver.k[layer], ver.v[layer], ks, kl, par, softcap=30.0,
+                        window=ver.window[layer])
+        ver.accept()
+        torch.cuda.synchronize()
+        got = [t.cpu().numpy() for t in (ver.argmax, ver.logprob, ver.accept_len, ver.path, ver.bonus)]
+        _check_sample(orc, ver.logits, ver.uniform.cpu().numpy(), ver.temperature.cpu().numpy(), par, draft, 6,
+                      ver.top_k.cpu().numpy(), ver.top_p.cpu().numpy(), ver.min_p.cpu().numpy(), got=got)
+        ver.commit()
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(ver.kv_len.cpu().numpy(), kl + 1 + got[2])
+
+
+def test_a_captured_step_replays_on_new_inputs():
+    ver, qkv, wq, wk, rng = _teacher(3)
+    twin, qkv2, wq2, wk2, _ = _teacher(3)
+    g = W.torch_generator(4, dev())
+    _new_inputs(ver, qkv, rng, g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    keep = [t.clone() for t in (*ver.k, *ver.v, ver.kv_len)]
+    with torch.cuda.stream(side):
+        _step(ver, qkv, wq, wk)  # warm-up
+    torch.cuda.synchronize()
+    for t, o in zip((*ver.k, *ver.v, ver.kv_len), keep):
+        t.copy_(o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _step(ver, qkv, wq, wk)
+    for _ in range(3):
+        _new_inputs(ver, qkv, rng, g)
+        for a, b in ((twin.parent, ver.parent), (twin.logits, ver.logits), (twin.draft, ver.draft),
+                     (twin.uniform, ver.uniform), *zip(qkv2, qkv)):
+            a.copy_(b)
+        graph.replay()
+        _step(twin, qkv2, wq2, wk2)
+        torch.cuda.synchronize()
+        for a, b in ((ver.argmax, twin.argmax), (ver.path, twin.path), (ver.bonus, twin.bonus), (ver.kv_len, twin.kv_len),
+                     (ver.logprob, twin.logprob), *zip(ver.out, twin.out), *zip(ver.k, twin.k), *zip(ver.v, twin.v)):
+            assert torch.equal(a, b)
+
+
+def test_step_from_host_with_a_sampling_teacher():
+    from tree_speculative_decoding_04_b200.verifier import TreeVerifier
+
+    rng = np.random.default_rng(6)
+    a, b = (TreeVerifier(2, 5, 4, 2, 64, 500, 2, 120, 5, softcap=50.0, sampling=True) for _ in range(2))
+    for ver in (a, b):
+        ver.kv_len.copy_(i32([60, 33]))
+        ver.top_k.fill_(20)
+    h = a.pinned_inputs()
+    par = parents(2, 5, 5, rng)
+    h["parent"].copy_(torch.as_tensor(par))
+    h["draft"].copy_(torch.as_tensor(rng.integers(0, 500, (2, 6)).astype(np.int32)))
+    h["logits"].copy_(torch.as_tensor(rng.normal(size=(2, 6, 500)).astype(np.float32)))
+    h["uniform"].copy_(torch.as_tensor(rng.random((2, 6)).astype(np.float32)))
+    for name in ("q", "tree_k", "tree_v"):
+        h[name].copy_(torch.as_tensor(rng.normal(size=tuple(h[name].shape))).to(torch.bfloat16))
+    a.step_from_host()
+    for name in ("parent", "draft", "logits", "tree_k", "tree_v"):
+        getattr(b, name).copy_(h[name])
+    b.uniform.copy_(h["uniform"])
+    for layer in range(2):
+        b.q[layer].copy_(h["q"][layer])
+        b.write_tree_rows(layer)
+    b.step()
+    torch.cuda.synchronize()
+    for x, y in ((a.argmax, b.argmax), (a.accept_len, b.accept_len), (a.path, b.path), *zip(a.out, b.out), *zip(a.k, b.k)):
+        assert torch.equal(x, y)
+    assert torch.equal(h["bonus"], b.bonus.cpu()) and a.h2d_bytes() == sum(
+        h[k].numel() * h[k].element_size() for k in ("parent", "draft", "logits", "uniform", "q", "tree_k", "tree_v"))
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Two attention and two sampling calls in flight together, each with a workspace of its own."""
+    q, k, v, ks, kl, par = _attn_case(2, 16, 8, 2, 128, [4000, 2500], 31)
+    ref, _ = _attend(q, k, v, ks, kl, par, softcap=50.0)
+    x, u, spar, draft, rng = _sample_case(4, 5, 30000, 32)
+    sref = _sample(x, u, [1.0] * 4, spar, draft, 9, p=[0.9] * 4)
+    _, anc, depth, status = gpu_mask(par, 1000)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs, wss = [torch.empty_like(q) for _ in streams], []
+    ks, kl = i32(ks), i32(kl)
+    torch.cuda.synchronize()
+    for s, out in zip(streams, outs):
+        wss.append(tv.attention_scored_workspace(2, 16, 8, 2, 128, k.shape[2], 0, q.device))
+        for _ in range(5):
+            tv.tree_attention_scored(q, k, v, ks, kl, anc, depth, status, out, wss[-1], softcap=50.0, stream=s)
+    got = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append(_sample(x, u, [1.0] * 4, spar, draft, 9, p=[0.9] * 4))
+    torch.cuda.synchronize()
+    for out in outs:
+        assert torch.equal(out, ref)
+    for g in got:
+        for a, b in zip(g[:5], sref[:5]):
+            np.testing.assert_array_equal(a, b)
+
+
+def test_attention_scored_workspace_is_needed_where_ranges_split():
+    q, k, v, ks, kl, par = _attn_case(1, 0, 4, 2, 64, 3000, 33)
+    _, anc, depth, status = gpu_mask(par, 10)
+    need = tv.attention_scored_workspace_size(1, 0, 4, 2, 64, k.shape[2], 0)
+    assert need > 0 and tv.attention_scored_workspace_size(1, 0, 4, 2, 64, k.shape[2], 64) == 0
+    for ws in (None, torch.empty(need - 16, dtype=torch.uint8, device=dev())):
+        with pytest.raises(tv.TVError, match="INVALID_ARG"):
+            tv.tree_attention_scored(q, k, v, i32(ks), i32(kl), anc, depth, status, torch.empty_like(q), ws)
+
+
+def test_attention_scored_wait_limit():
+    """Waits that give up at once: every sequence is either flagged, with rows that are zero or right, or right."""
+    q, k, v, ks, kl, par = _attn_case(3, 40, 8, 2, 128, [2000, 900, 50], 34)
+    ref, _ = _attend(q, k, v, ks, kl, par, softcap=50.0)
+    tv.set_wait_limit_ns(1)
+    try:
+        out, status = _attend(q, k, v, ks, kl, par, softcap=50.0)
+    finally:
+        tv.set_wait_limit_ns(0)
+    for b in range(3):
+        assert int(status[b]) in (0, tv.SEQ_TIMEOUT)
+        same, zero = (out[b] == ref[b]).all(-1), (out[b] == 0).all(-1)
+        assert bool((same | zero).all()) if int(status[b]) else bool(same.all())
+    again, status = _attend(q, k, v, ks, kl, par, softcap=50.0)
+    assert torch.equal(again, ref) and int(status.abs().sum()) == 0

@@ -19,6 +19,7 @@ from ._lib import (  # noqa: F401
     TVError,
     accept_sample_workspace,
     attention_scored_workspace,
+    attention_scored_workspace_size,
     attention_workspace,
     kv_commit_realign,
     layer_pointers,

@@ -314,11 +314,17 @@ def tree_accept_lm_head(hidden, w_lm, draft, parent, depth, anc_mask, status, ma
     _check(rc, "tree_accept_lm_head")
 
 
+def attention_scored_workspace_size(B, M, Hq, Hkv, D, S_cap, window) -> int:
+    """Bytes of device scratch tree_attention_scored needs for this shape on the
+    current device (0 = none: key ranges are not split)."""
+    return int(load().tree_attention_scored_workspace_size(B, M, Hq, Hkv, D, int(S_cap), int(window)))
+
+
 def attention_scored_workspace(B, M, Hq, Hkv, D, S_cap, window, device) -> torch.Tensor | None:
     """A device buffer of tree_attention_scored_workspace_size bytes for this shape
     (None when no workspace is needed).  Calls that may overlap need one each."""
     with torch.cuda.device(device):
-        nbytes = int(load().tree_attention_scored_workspace_size(B, M, Hq, Hkv, D, int(S_cap), int(window)))
+        nbytes = attention_scored_workspace_size(B, M, Hq, Hkv, D, S_cap, window)
     if nbytes == 0:
         return None
     return torch.empty((nbytes + 15) // 16 * 16, dtype=torch.uint8, device=device)

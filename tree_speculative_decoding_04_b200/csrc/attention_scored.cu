@@ -378,12 +378,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh->tmem;
   const uint64_t lim = p.wait_limit_ns;
-  // Waits for a role's `n`-th item.  An item list is short of nothing the GPU has to
-  // wait for, so this wait keeps the full limit; if it runs out, the role stops.
+  // Waits for a role's `n`-th item.  A role that gives up on a wait of its own still
+  // takes its items, so the next one comes once every reader is through with the one
+  // before the last: warp 1 waits for that longer than a reader's own waits can add
+  // up to, and the readers longer than warp 1, so that all of them see the same list.
+  constexpr uint64_t kListWait = 8 * kWaitLimitNs;
   auto next_item = [&](int n) -> Item {
     Item it = {};
     it.index = -1;
-    if (mbar_wait(&sh->item_full[n & 1], (n >> 1) & 1)) it = sh->item[n & 1];
+    if (mbar_wait(&sh->item_full[n & 1], (n >> 1) & 1, 4 * kListWait)) it = sh->item[n & 1];
     return it;
   };
   // Ring order of an item's tiles: K_0 (and K_1 where the pipes take turns), then
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // -------------------------------------------------------------- items
       for (int n = 1;; ++n) {
         const Item it = decode(blockIdx.x + n * gridDim.x, false);
-        if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sh->item_empty[n & 1], ((n >> 1) - 1) & 1))) break;
+        if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sh->item_empty[n & 1], ((n >> 1) - 1) & 1, kListWait))) break;
         if (lane == 0) {
           sh->item[n & 1] = it;
           mbar_arrive(&sh->item_full[n & 1]);

@@ -78,13 +78,23 @@ class StepResult:
 
 class TreeVerifier:
     def __init__(self, B, M, Hq, Hkv, D, V, L, S_cap, max_depth, realign=False, device="cuda",
-                 k_layers=None, v_layers=None, with_mask_outputs=None, commit_layers=None, rope_theta=0.0):
+                 k_layers=None, v_layers=None, with_mask_outputs=None, commit_layers=None, rope_theta=0.0,
+                 softcap=0.0, window=0, alibi_slopes=None, sampling=False):
         """k_layers / v_layers: the L per-layer caches (default: allocated here).
         commit_layers: the indices of the layers kv_commit_realign moves (default
         all); a caller whose layer list repeats a buffer commits each buffer once.
         rope_theta > 0: q and the tree rows' K are given before their rotary
         embedding; the kernels rotate them to the tree positions kv_len + depth
-        (tree_kv_write for K, tree_attention's query staging for q)."""
+        (tree_kv_write for K, tree_attention's query staging for q).
+        softcap, window (one for all layers, or a sequence with one for each), alibi_slopes
+        (fp32 [Hq]): the teacher's scores, see tree_attention_scored.  Its queries
+        are taken as they are: rotate them before, or fill q and the cache with
+        norm_rope().
+        sampling: the accepted tokens are drawn instead of the argmax (see
+        tree_accept_sample), with the random numbers `uniform` [B][M+1] and the
+        settings `temperature`, `top_k`, `top_p`, `min_p` [B] (1, off, off, off
+        until the caller writes them); the draws are `argmax` (the token at every
+        node) and `logprob`."""
         self.B, self.M, self.Hq, self.Hkv, self.D, self.V, self.L = B, M, Hq, Hkv, D, V, L
         self.S_cap, self.max_depth, self.realign = S_cap, max_depth, bool(realign)
         self.rope_theta = float(rope_theta)
@@ -115,8 +125,26 @@ class TreeVerifier:
         ids = list(range(L)) if commit_layers is None else list(commit_layers)
         self.k_commit_ptrs = tv.layer_pointers([self.k[i] for i in ids], dev)
         self.v_commit_ptrs = tv.layer_pointers([self.v[i] for i in ids], dev)
-        self.workspace = tv.attention_workspace(B, M, Hq, Hkv, D, S_cap, dev)
+        self.softcap, self.alibi_slopes = float(softcap), alibi_slopes
+        self.window = [int(window)] * L if isinstance(window, int) else [int(w) for w in window]
+        if len(self.window) != L:
+            raise tv.TVError(f"window: {len(self.window)} entries for {L} layers")
+        self.scored = [self.softcap > 0 or w > 0 or alibi_slopes is not None for w in self.window]
+        if self.rope_theta > 0 and any(self.scored):
+            raise tv.TVError("rope_theta: capped, windowed and biased attention take rotated queries (see norm_rope)")
+        self.workspace = None if all(self.scored) else tv.attention_workspace(B, M, Hq, Hkv, D, S_cap, dev)
+        scored_ws = [tv.attention_scored_workspace(B, M, Hq, Hkv, D, S_cap, w, dev)
+                     for w in sorted({w for w, on in zip(self.window, self.scored) if on})]
+        self.scored_workspace = max((w for w in scored_ws if w is not None), key=lambda w: w.numel(), default=None)
         self.argmax = torch.zeros((B, self.n), **i32)
+        self.sampling = bool(sampling)
+        if self.sampling:
+            f32 = dict(dtype=torch.float32, device=dev)
+            self.uniform = torch.zeros((B, self.n), **f32)
+            self.temperature, self.top_p = torch.ones((B,), **f32), torch.ones((B,), **f32)
+            self.min_p, self.top_k = torch.zeros((B,), **f32), torch.zeros((B,), **i32)
+            self.logprob = torch.zeros((B, self.n), **f32)
+            self.sample_workspace = tv.accept_sample_workspace(B, M, V, dev)
         # accept results side by side, so that they come back in one copy
         nres = B + B * (max_depth + 1) + B
         self._results = torch.zeros((nres,), **i32)
@@ -132,9 +160,12 @@ class TreeVerifier:
 
     # ------------------------------------------------------------------ device path
     def launches_per_step(self) -> int:
-        """Kernels this library launches per step(): mask 1, attention 1 per layer,
-        accept 2, commit 2 (step_from_host adds one tree_kv_write per layer)."""
-        return 1 + self.L + 2 + 2
+        """Kernels this library launches per step(): mask 1, attention 1 per layer
+        (2 where a scored layer's key ranges may be split), accept 2 (5 with
+        sampling), commit 2 (step_from_host adds one tree_kv_write per layer)."""
+        split = sum(on and tv.attention_scored_workspace_size(self.B, self.M, self.Hq, self.Hkv, self.D, self.S_cap, w) > 0
+                    for w, on in zip(self.window, self.scored))
+        return 1 + self.L + split + (5 if self.sampling else 2) + 2
 
     def build_mask(self, stream=None):
         tv.tree_build_mask(self.parent, self.max_depth, self.anc, self.depth, self.status, stream)
@@ -145,10 +176,23 @@ class TreeVerifier:
         (true after tree_build_mask, tree_kv_write and the attention of another
         layer; false after kv_commit_realign), so prefix tiles may stream while
         it finishes.  Off by default: on B200 it measured no faster."""
+        if self.scored[layer]:
+            tv.tree_attention_scored(self.q[layer], self.k[layer], self.v[layer], self.kv_start, self.kv_len, self.anc,
+                                     self.depth, self.status, self.out[layer], self.scored_workspace,
+                                     softcap=self.softcap, window=self.window[layer], alibi_slopes=self.alibi_slopes,
+                                     stream=stream)
+            return
         flags = (tv.ATTN_PREFIX_READY if prefix_ready else 0) | (tv.ATTN_ROPE if self.rope_theta > 0 else 0)
         tv.tree_attention(self.q[layer], self.k[layer], self.v[layer], self.kv_start, self.kv_len, self.anc,
                           self.status, self.out[layer], self.workspace, stream=stream, flags=flags,
                           depth=self.depth, rope_theta=self.rope_theta)
+
+    def norm_rope(self, layer, qkv, q_weight, k_weight, stream=None, **how):
+        """The packed projection rows of one layer (bf16 [B][M+1][Hq + 2 Hkv][D]) ->
+        this layer's queries and tree rows in the cache (see tree_qk_norm_rope;
+        `how`: eps, weight_offset, rope_theta, rotary_dim)."""
+        tv.tree_qk_norm_rope(qkv, q_weight, k_weight, self.q[layer], self.k[layer], self.v[layer], self.kv_start,
+                             self.kv_len, self.depth, stream=stream, **how)
 
     def write_tree_rows(self, layer, stream=None):
         """tree_k / tree_v of one layer -> the cache, behind each sequence's prefix."""
@@ -158,6 +202,12 @@ class TreeVerifier:
                          depth=self.depth if self.rope_theta > 0 else None, rope_theta=self.rope_theta)
 
     def accept(self, stream=None):
+        if self.sampling:
+            tv.tree_accept_sample(self.logits, self.uniform, self.temperature, self.draft, self.parent, self.depth,
+                                  self.anc, self.status, self.max_depth, self.argmax, self.accept_len, self.path,
+                                  self.bonus, self.sample_workspace, top_k=self.top_k, top_p=self.top_p,
+                                  min_p=self.min_p, logprob=self.logprob, stream=stream)
+            return
         tv.tree_accept(self.logits, self.draft, self.parent, self.depth, self.anc, self.status, self.max_depth,
                        self.argmax, self.accept_len, self.path, self.bonus, stream)
 
@@ -192,7 +242,7 @@ class TreeVerifier:
     def pinned_inputs(self):
         """Pinned host staging buffers (allocated once): parent, draft, logits,
         q [L][B][M+1][Hq][D], tree_k / tree_v [L][B][Hkv][M+1][D] for the inputs;
-        accept_len, path, bonus for the results."""
+        uniform with sampling; accept_len, path, bonus for the results."""
         if self._host is None:
             buf = torch.zeros(self.layout.nbytes, dtype=torch.uint8, pin_memory=True)
             res = torch.zeros(self._results.shape, dtype=torch.int32, pin_memory=True)
@@ -200,12 +250,15 @@ class TreeVerifier:
             h = self.layout.views(buf)
             h.update(_buf=buf, _res=res, accept_len=res[:B], path=res[B:B + B * (md + 1)].view(B, md + 1),
                      bonus=res[B + B * (md + 1):])
+            if self.sampling:
+                h["uniform"] = torch.zeros(self.uniform.shape, dtype=torch.float32, pin_memory=True)
             self._host = h
         return self._host
 
     def h2d_bytes(self) -> int:
         lay = self.layout
-        return lay.meta_bytes + lay.logits_bytes + lay.L * (lay.q_bytes + 2 * lay.rows_bytes)
+        draws = self.uniform.numel() * 4 if self.sampling else 0
+        return lay.meta_bytes + lay.logits_bytes + lay.L * (lay.q_bytes + 2 * lay.rows_bytes) + draws
 
     def d2h_bytes(self) -> int:
         return self._results.numel() * 4
@@ -236,6 +289,8 @@ class TreeVerifier:
                 ev[1 + layer].record(cs)
             o = lay.logits_off
             dst[o:o + lay.logits_bytes].copy_(src[o:o + lay.logits_bytes], non_blocking=True)
+            if self.sampling:
+                self.uniform.copy_(h["uniform"], non_blocking=True)
             ev[1 + self.L].record(cs)
         with torch.cuda.stream(s):
             s.wait_event(ev[0])
