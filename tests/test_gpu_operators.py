@@ -575,3 +575,22 @@ def test_attention_scored_wait_limit():
         assert bool((same | zero).all()) if int(status[b]) else bool(same.all())
     again, status = _attend(q, k, v, ks, kl, par, softcap=50.0)
     assert torch.equal(again, ref) and int(status.abs().sum()) == 0
+
+
+@pytest.mark.parametrize("M,Hq,lens", [(0, 32, [3431, 583, 935, 3652, 609, 1846, 579, 3760]), (16, 64, [3000, 1500, 700]),
+                                       (40, 16, [2500, 90])])
+def test_attention_scored_thousands_of_launches(M, Hq, lens):
+    """Lone and paired query tiles over split ranges, queued thousands deep: one answer, no sequence flagged.  (The
+    two pipes of a lone tile run apart by as much as the ring of key tiles allows.)"""
+    B = len(lens)
+    q, k, v, ks, kl, par = _attn_case(B, M, Hq, 8 if M == 0 else 2, 128, lens, 77)
+    ref, _ = _attend(q, k, v, ks, kl, par, softcap=50.0)
+    _check_attn(ref, q, k, v, ks, kl, par, softcap=50.0)
+    _, anc, depth, status = gpu_mask(par, 1000)
+    ks, kl = i32(ks), i32(kl)
+    ws = tv.attention_scored_workspace(B, M, Hq, k.shape[1], 128, k.shape[2], 0, q.device)
+    out = torch.empty_like(q)
+    for _ in range(6):
+        for _ in range(3000):
+            tv.tree_attention_scored(q, k, v, ks, kl, anc, depth, status, out, ws, softcap=50.0)
+        assert int(status.abs().sum()) == 0 and torch.equal(out, ref)

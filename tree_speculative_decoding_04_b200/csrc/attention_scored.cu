@@ -464,14 +464,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it.nt == 0 || !ok) continue;
         const bool dual = it.dual;
         const int steps = dual ? it.nt : (it.nt + 1 - q) / 2;
-        // a slot is free once both pipes have read it, or its one reader has
-        auto release = [&](uint32_t s) {
-          tc_commit(&sh->empty[s]);
-          if (!dual) tc_commit(&sh->empty[s]);
+        // Each pipe waits for every entry of the ring in its order, the other pipe's as
+        // well: a barrier's parity tells a landed copy from a pending one only to who
+        // has seen the slot's copy before.  A slot is free once both pipes are through
+        // with it: with their products, or by having seen that it is the other's.
+        const int la = dual ? 1 : 2;
+        int seen = 0, kj = 0, vj = 0;
+        auto see = [&](int entry) -> bool {
+          for (; seen <= entry; ++seen) {
+            const uint32_t idx = base + seen, s = idx % kSlots;
+            if (!mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim)) return false;
+            const bool is_k = kj < it.nt && kj - vj < la;
+            const int j = is_k ? kj++ : vj++;
+            if (!dual && (j & 1) != q) mbar_arrive(&sh->empty[s]);
+          }
+          return true;
         };
         auto qk = [&](int i) -> bool {
-          const uint32_t idx = base + k_idx(it, dual ? i : 2 * i + q), s = idx % kSlots, st = step0 + i;
-          if (!mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim)) return false;
+          const int entry = k_idx(it, dual ? i : 2 * i + q);
+          const uint32_t s = (base + entry) % kSlots, st = step0 + i;
+          if (!see(entry)) return false;
           if (st > 0 && !mbar_wait(&sh->s_free[q], (st - 1) & 1, lim)) return false;
           tc_fence_after();
           const uint64_t da = sw128_desc(smem_u32(q_s + (dual ? q : 0) * kQTile), 16);
@@ -481,14 +493,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ss(t_q, da + (uint64_t)((k >> 2) * (kQHalf / 16) + (k & 3) * 2),
                    db + (uint64_t)((k >> 2) * (kHalf / 16) + (k & 3) * 2), idesc_s, k > 0 ? 1u : 0u);
           tc_commit(&sh->s_full[q]);
-          release(s);
+          tc_commit(&sh->empty[s]);
           return true;
         };
         ok = mbar_wait(&sh->q_full, busy & 1, lim) && (steps == 0 || qk(0));
         for (int i = 0; i < steps && ok; ++i) {
           if (i + 1 < steps && !(ok = qk(i + 1))) break;
-          const uint32_t idx = base + v_idx(it, dual ? i : 2 * i + q), s = idx % kSlots;
-          ok = mbar_wait(&sh->full[s], (idx / kSlots) & 1, lim) && mbar_wait(&sh->p_full[q], (step0 + i) & 1, lim);
+          const int entry = v_idx(it, dual ? i : 2 * i + q);
+          const uint32_t s = (base + entry) % kSlots;
+          ok = see(entry) && mbar_wait(&sh->p_full[q], (step0 + i) & 1, lim);
           if (!ok) break;
           tc_fence_after();
           const uint64_t db = sw128_desc(smem_u32(ring + s * kTile), kHalf);
@@ -497,8 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ts(t_q + kColO, t_q + kColP + k * 8, db + (uint64_t)(k * (16 * 128 / 16)), idesc_o,
                    (i > 0 || k > 0) ? 1u : 0u);
           tc_commit(&sh->pv_done[q]);
-          release(s);
+          tc_commit(&sh->empty[s]);
         }
+        ok = ok && see(2 * it.nt - 1);
         if (!ok) atomicExch(&sh->failed, 1);
         ++busy;
         base += 2 * it.nt;
@@ -927,7 +941,7 @@ __global__ void __launch_bounds__(256) scored_merge_kernel(const __grid_constant
   __shared__ int red[8];
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int len = p.plan[0];
+  const int len = __ldcg(p.plan);
   const float4* ws_o = reinterpret_cast<const float4*>(p.ws_o);
   const int qt = blockIdx.x % p.nqt, hk = blockIdx.x / p.nqt % p.Hkv, b = blockIdx.x / p.nqt / p.Hkv;
   const int nr = ranges_of(sequence(p, b).nt, len);
