@@ -553,9 +553,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (gr < p.rows && (dual || k < kN / 2))
           v[k] = __ldg(reinterpret_cast<const uint4*>(p.q + query_row(p, b, hk, gr) * D) + c);
       }
-      for (int i = 0; i < p.W; ++i) sh->anc[stid][i] = __ldg(p.anc + ((int64_t)b * (p.M + 1) + u) * p.W + i);
-      if (p.depth)
-        for (int i = stid; i <= p.M; i += 256) sh->depth[i] = (uint8_t)__ldg(p.depth + (int64_t)b * (p.M + 1) + i);
+      constexpr int kW = kMaxRows / 32;
+      uint32_t a[kW];
+      const int64_t node = (int64_t)b * (p.M + 1) + u;
+#pragma unroll
+      for (int i = 0; i < kW; ++i) a[i] = i < p.W ? __ldg(p.anc + node * p.W + i) : 0u;
+      const int d = p.depth && stid <= p.M ? __ldg(p.depth + (int64_t)b * (p.M + 1) + stid) : 0;
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
         const int row = r0 + k * kStep, rr = row & (kQRows - 1);
@@ -563,6 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(q_s + (row / kQRows) * kQTile + (c >> 3) * kQHalf + rr * 128 +
                                     (((c & 7) ^ (rr & 7)) << 4)) = v[k];
       }
+#pragma unroll
+      for (int i = 0; i < kW; ++i) sh->anc[stid][i] = a[i];
+      if (stid <= p.M) sh->depth[stid] = (uint8_t)d;
       fence_async_smem();
       tc_fence_before();
       asm volatile("bar.sync 3, 256;" ::: "memory");
