@@ -57,9 +57,8 @@ constexpr int kColP = kKeys, kColO = 128;
 // small one, and 2^24 leaves both far from their limits).
 constexpr float kGrow = 24.0f;
 constexpr int kMaxBatch = 4096;
-constexpr int kMaxRounds = 6;              // items per SM, at most, where ranges are split
-constexpr int kMinSplitTiles = 6;          // key tiles below which a range is not split further
-constexpr int kMaxRankedRows = kThreads;
+constexpr int kMinTiles = 6;               // no cut nearer to a row's ends than this many key tiles
+constexpr int kSecondItem = 6;             // what a CTA's second item costs on top, in key tiles
 
 // Which scores an instance computes.
 //   kCapLow: capped with cap * log2e <= kLowCap: every exponent lies within that of
@@ -86,17 +85,15 @@ struct ScoredParams {
   int rows;         // G * (M + 1) query rows of a (sequence, kv head)
   int nqt, npairs;  // query tiles, and items' pairs of them
   int rec_rows;     // rows of a partial record
-  int64_t max_items;
-  int split;        // key ranges may be split over items
-  int cand_step;    // range lengths tried: kMinSplitTiles + i * cand_step tiles
+  int grid;         // CTAs
   float inv_g;      // 1 / G
   float scale_log2, ref;
   float c[5];       // capped score = x * (c0 + c1 x^2 + ...), x = q.k
   float x_lim, z2, cap_log2;  // |x| of the polynomial's range; e^2z = 2^(z2 x); cap * log2e
   uint64_t wait_limit_ns;
-  int* plan;        // [0]: key tiles per range, for the merge
-  float* ws_o;      // records [item][pipe][D / 4][rec_rows] float4
-  float2* ws_ml;    // [item][pipe][rec_rows] (reference, sum)
+  float* ws_o;      // records [CTA][0: cut at its start, 1: only at its end][pipe][D / 4][rec_rows] float4
+  float2* ws_ml;    // [CTA][2][pipe][rec_rows] (reference, sum)
+  int2* ws_row;     // [row of work] the first and the last CTA with a piece; (-1, -1): one had it all
 };
 
 // A sequence's place in the cache, the first key that its root sees and the key
@@ -118,12 +115,57 @@ __device__ __forceinline__ Geo sequence(const ScoredParams& p, int b) {
   return g;
 }
 
-__device__ __forceinline__ int ranges_of(int nt, int len) { return nt <= len ? 1 : (nt + len - 1) / len; }
+// How the work is dealt.  The rows of work are the pairs of query tiles of every
+// (sequence, kv head), in this order.  The CTAs take consecutive shares of them, so a
+// row may be cut between CTAs; the pieces are joined by the merge kernel.
+//   by cost  (per = 0) a row costs its key tiles, twice for a full pair (a lone query
+//            tile takes half the time), and every CTA takes the same cost
+//   by piece (per > 0) a row makes equal pieces of at most `per` key tiles, and every
+//            CTA takes one piece
+// A share by cost crosses from row to row, and every further item costs the filling and
+// draining of the pipes and an epilogue; pieces are uneven.  So: pieces where there is a
+// CTA for every row and the longest piece is no longer than an even share and kSecondItem
+// tiles, and cost elsewhere.
+__device__ __forceinline__ int tiles_of(int nt) { return max(nt, 1); }  // (a sequence without keys has rows to zero)
+
+struct Shares {  // (the host has checked that all of it fits in 31 bits)
+  int total, even;      // all rows, in the unit of the shares; a CTA's share,
+  int extra, ctas;      // plus one for the first `extra`; CTAs that take part
+  int per, head, pair;  // of one unit of a row: units of its kv head and of a full pair
+  // `units`: the sum of units_of over the sequences
+  __device__ __forceinline__ void set(const ScoredParams& p, int units, int per_) {
+    per = per_;
+    head = per ? p.npairs : p.nqt;
+    pair = per ? 1 : 2;
+    total = units * p.Hkv * head;
+    ctas = total;
+    // (at least two units by cost, so that every border inside a row is a cut of its own)
+    if (!per && p.nqt > 1) ctas = max(1, min(total / 2, max(total / (2 * kMinTiles), p.B * p.Hkv * p.npairs)));
+    if (!per && p.nqt == 1) ctas = max(total / kMinTiles, p.B * p.Hkv);
+    ctas = min(p.grid, ctas);
+    even = (uint32_t)total / (uint32_t)ctas;
+    extra = total - even * ctas;
+  }
+  __device__ __forceinline__ int units_of(int nt) const {
+    return per ? (int)((uint32_t)(nt + per - 1) / (uint32_t)per) : nt;
+  }
+  __device__ __forceinline__ int begin(int cta) const { return even * cta + min(cta, extra); }
+  // the key tile at which a row of nt tiles, n units, that begins at `start` is cut for a border
+  __device__ __forceinline__ int cut(int border, int start, int nt, int n, bool dual) const {
+    const int d = border - start;
+    if (d <= 0) return 0;
+    if (per) return d >= n ? nt : (int)((uint64_t)nt * d / n);
+    const int t = dual ? (d + 1) >> 1 : d;
+    if (t >= nt) return nt;
+    if (nt < 2 * kMinTiles) return 2 * t < nt ? 0 : nt;
+    return t < kMinTiles ? 0 : (nt - t < kMinTiles ? nt : t);
+  }
+};
 
 // One item: a pair of query tiles (or a last one alone) and a range of key tiles.
 struct Item {
   int index;  // -1: no more
-  int b, hk, qt0, dual, nr;  // nr: ranges of the sequence
+  int b, hk, qt0, dual, whole, rec;  // whole: the range is all of the row; else its record
   int kl, first, sl;         // first: the range's first key
   int nt;                    // key tiles (0: nothing to compute, zero rows)
   int row0;                  // cache column of the first key
@@ -134,12 +176,10 @@ struct Shared {
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full;
   uint64_t item_full[2], item_empty[2];
   uint64_t drain;
-  unsigned long long best;
   uint32_t tmem;
   int failed;
   Item item[2];
   float2 join_ml[kQRows];
-  uint16_t order[kMaxRankedRows];
   uint8_t depth[kMaxRows];
   uint32_t anc[2 * kQRows][kMaxRows / 32 + 1];  // ancestor words of the softmax threads' rows
 };
@@ -237,7 +277,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     sh->failed = 0;
-    sh->best = ~0ull;
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], 2);
@@ -266,11 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait_primary();
   pdl_launch_dependents();
 
-  // ---------------------------------------------------------------- the plan
-  // Every CTA forms the same plan from the sequences' lengths: the number of key
-  // tiles per range that finishes first by this estimate, in steps of a pipe
-  // pair: the items of a CTA one after another, 4 steps of set-up and epilogue
-  // each, 4 for the merge where ranges are split.  Each thread tries one length.
+  // ---------------------------------------------------------------- the CTA's share
   int* nt_s = reinterpret_cast<int*>(ring);
   int4* geo_s = reinterpret_cast<int4*>(ring + 4 * kMaxBatch);
   for (int b = tid; b < p.B; b += kThreads) {
@@ -280,97 +315,139 @@ __global__ void __launch_bounds__(kThreads, 1)
     geo_s[b] = make_int4(g.sl, g.ks, g.kl, st);
   }
   __syncthreads();
-  int len = INT_MAX;
-  const int per_range = p.Hkv * p.npairs;  // items of one key range of a sequence
-  if (p.split) {
-    const int l = kMinSplitTiles + tid * p.cand_step;
-    // ceil(nt / l) by a reciprocal: exact for nt < 2^21, which the host's limit on
-    // split ranges ensures
-    const float inv = 1.f / (float)l, up = (float)l - 0.5f;
-    int64_t ranges = 0;
-    for (int b = 0; b < p.B; ++b) ranges += max(1, (int)(((float)nt_s[b] + up) * inv));
-    const int64_t items = ranges * per_range;
-    unsigned long long key = ~0ull;
-    if (items <= p.max_items) {
-      const int64_t steps = p.nqt > 1 ? l : (l + 1) / 2;
-      const int64_t rounds = (items + gridDim.x - 1) / gridDim.x;
-      // a lone query tile takes half the steps of a pair
-      const int64_t mean = (ranges * p.Hkv * p.nqt * l) / (2 * gridDim.x);
-      const int64_t est = min(rounds * steps, mean + steps) + 4 * rounds + (ranges > p.B ? 4 : 0);
-      key = (unsigned long long)est << 32 | (uint32_t)~l;  // the longest of equal ones
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) key = min(key, __shfl_xor_sync(0xffffffffu, key, off));
-    if (lane == 0) atomicMin(&sh->best, key);
-    __syncthreads();
-    len = (int)~(uint32_t)sh->best;
-    if (blockIdx.x == 0 && tid == 0) p.plan[0] = len;
-  }
-  // Whole sequences in several rounds: the longest first.
-  const bool ranked = !p.split && p.max_items > (int64_t)gridDim.x && p.B <= kMaxRankedRows;
-  if (ranked) {
-    if (tid < p.B) {
-      int r = 0;
-      for (int b = 0; b < p.B; ++b) r += nt_s[b] > nt_s[tid] || (nt_s[b] == nt_s[tid] && b < tid);
-      sh->order[r] = (uint16_t)tid;
-    }
-    __syncthreads();
-  }
-  // Item `index`, by warp 1; the first one reads the plan's scratch.
   const bool aligned_ok = (smem_u32(smem) & 1023u) == 0;  // the swizzled tiles need it (else all sequences fail)
-  auto decode = [&](int index, bool scratch) -> Item {
+  // Warp 1 walks the rows of the share.  Its place: a sequence with its geometry and
+  // status, the units of the sequences before it, and the row inside the sequence.
+  struct Place {
+    int before, lo, hi;  // units of earlier sequences; the share
+    int b, hk, pair, count;
+    bool fresh;          // g and st are of another sequence
+    Geo g;
+    int st, n;           // units of a row
+  } at = {};
+  Shares shares = {};
+  // The next item of the share.
+  auto next = [&]() -> Item {
     Item it = {};
     it.index = -1;
-    int base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int i = b0 + lane;
-      const int b = i < p.B ? (ranked ? sh->order[i] : i) : 0;
-      const int cnt = i < p.B ? ranges_of(scratch ? nt_s[b] : sequence(p, b).nt, len) * per_range : 0;
-      int incl = cnt;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += o;
+    while (at.b < p.B && at.before * p.Hkv * shares.head < at.hi) {
+      if (at.fresh) {
+        at.st = __ldcg(p.status + at.b);
+        at.g = sequence(p, at.b);
+        at.n = shares.units_of(tiles_of(at.g.nt));
+        at.fresh = false;
       }
-      const unsigned m = __ballot_sync(0xffffffffu, index < base + incl);
-      if (m) {
-        const int src = __ffs(m) - 1;
-        it.b = __shfl_sync(0xffffffffu, b, src);
-        const int rem = index - __shfl_sync(0xffffffffu, base + incl - cnt, src);
-        Geo g;
-        int st;
-        if (scratch) {
-          const int4 v = geo_s[it.b];
-          g = Geo{v.x, v.y, v.z, 0, nt_s[it.b]};
-          g.first = p.window > 0 ? max(0, g.kl - (p.window - 1)) : 0;
-          st = v.w;
-        } else {
-          g = sequence(p, it.b);
-          st = __ldcg(p.status + it.b);
+      const int nt = tiles_of(at.g.nt);
+      const bool dual = 2 * at.pair + 1 < p.nqt;
+      const int start = at.before * p.Hkv * shares.head + at.n * (at.hk * shares.head + at.pair * shares.pair);
+      if (start >= at.hi) break;
+      const int t0 = shares.cut(at.lo, start, nt, at.n, dual), t1 = shares.cut(at.hi, start, nt, at.n, dual);
+      if (t0 < t1) {
+        it.index = at.count++;
+        it.b = at.b;
+        it.hk = at.hk;
+        it.qt0 = 2 * at.pair;
+        it.dual = dual;
+        it.whole = t0 == 0 && t1 == nt;
+        it.rec = 2 * (2 * blockIdx.x + (t0 > 0 ? 0 : 1));
+        it.sl = at.g.sl;
+        it.kl = at.g.kl;
+        it.first = at.g.first + t0 * kKeys;
+        it.row0 = at.g.ks + it.first;
+        it.nt = aligned_ok && at.st == 0 && at.g.nt > 0 ? t1 - t0 : 0;
+        if (p.ws_row && lane == 0) {
+          int2* row = p.ws_row + ((int64_t)at.b * p.Hkv + at.hk) * p.npairs + at.pair;
+          if (t0 == 0) __stcg(&row->x, it.whole ? -1 : (int)blockIdx.x);
+          if (t1 == nt) __stcg(&row->y, it.whole ? -1 : (int)blockIdx.x);
         }
-        it.index = index;
-        it.nr = ranges_of(g.nt, len);
-        it.qt0 = 2 * (rem % p.npairs);
-        it.dual = it.qt0 + 1 < p.nqt;
-        const int range = rem / p.npairs % it.nr;
-        it.hk = rem / p.npairs / it.nr;
-        const int per = (g.nt + it.nr - 1) / it.nr;
-        it.sl = g.sl;
-        it.kl = g.kl;
-        it.first = g.first + range * per * kKeys;
-        it.row0 = g.ks + it.first;
-        it.nt = aligned_ok && st == 0 ? max(0, min(per, g.nt - range * per)) : 0;
-        return it;
       }
-      base += __shfl_sync(0xffffffffu, incl, 31);
+      if (++at.pair == p.npairs) {
+        at.pair = 0;
+        if (++at.hk == p.Hkv) {
+          at.hk = 0;
+          at.before += at.n;
+          ++at.b;
+          at.fresh = true;
+        }
+      }
+      if (t0 < t1) break;
     }
     return it;
   };
   if (warp == 1) {
-    const Item it = decode(blockIdx.x, true);
-    if (lane == 0) sh->item[0] = it;
+    int tiles = 0, longest = 0;
+    for (int b = lane; b < p.B; b += 32) {
+      tiles += tiles_of(nt_s[b]);
+      longest = max(longest, tiles_of(nt_s[b]));
+    }
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    const int heads = p.Hkv * p.npairs;
+    int per = 0, units = tiles;
+    if (p.B * heads <= p.grid) {
+      per = longest;
+      units = p.B;
+      if (p.ws_row) {
+        // the shortest pieces, of 32 lengths from an even share on, that the CTAs can take
+        const int least = max(kMinTiles, (int)((uint32_t)(tiles * heads + p.grid - 1) / (uint32_t)p.grid));
+        const int mine = least + lane * ((least + 15) >> 4);
+        int n = 0;
+#pragma unroll 4
+        for (int b = 0; b < p.B; ++b) n += (uint32_t)(tiles_of(nt_s[b]) + mine - 1) / (uint32_t)mine;
+        const unsigned m = __ballot_sync(0xffffffffu, n * heads <= p.grid);
+        if (m) {
+          per = __shfl_sync(0xffffffffu, mine, __ffs(m) - 1);
+          units = __shfl_sync(0xffffffffu, n, __ffs(m) - 1);
+        }
+        const int full = p.nqt > 1 ? 2 : 1;
+        if ((int64_t)full * (min(per, longest) - kSecondItem) * p.grid > tiles * p.Hkv * p.nqt) {
+          per = 0;
+          units = tiles;
+        }
+      }
+    }
+    shares.set(p, units, per);
+    // the sequence in which the share begins
+    at.b = p.B;
+    if ((int)blockIdx.x < shares.ctas) {
+      at.lo = shares.begin(blockIdx.x);
+      at.hi = shares.begin(blockIdx.x + 1);
+      const int seq = p.Hkv * shares.head;
+      int before = 0;
+      for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int own = b < p.B ? shares.units_of(tiles_of(nt_s[b])) : 0;
+        int incl = own;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, incl, off);
+          if (lane >= off) incl += o;
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, b < p.B && (before + incl) * seq > at.lo);
+        if (m) {
+          const int src = __ffs(m) - 1;
+          at.b = b0 + src;
+          at.before = __shfl_sync(0xffffffffu, before + incl - own, src);
+          at.n = __shfl_sync(0xffffffffu, own, src);
+          const int4 v = geo_s[at.b];
+          at.g = Geo{v.x, v.y, v.z, 0, nt_s[at.b]};
+          at.g.first = p.window > 0 ? max(0, at.g.kl - (p.window - 1)) : 0;
+          at.st = v.w;
+          // the kv head, and the pair, in which it begins
+          const uint32_t inside = at.lo - at.before * seq;
+          at.hk = inside / (uint32_t)(at.n * shares.head);
+          at.pair = (inside - at.hk * at.n * shares.head) / (uint32_t)(at.n * shares.pair);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    const Item it = next();
+    if (lane == 0) {
+      sh->item[0] = it;
+      mbar_arrive(&sh->item_full[0]);
+    }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh->item_full[0]);
   }
   fence_async_smem();  // the plan's scratch lies in the ring, which the copies write next
   tc_fence_before();
@@ -402,9 +479,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     if (warp == 1) {
       // -------------------------------------------------------------- items
+      bool stuck = false;
       for (int n = 1;; ++n) {
-        const Item it = decode(blockIdx.x + n * gridDim.x, false);
-        if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(&sh->item_empty[n & 1], ((n >> 1) - 1) & 1, kListWait))) break;
+        const Item it = next();
+        if (n >= 2 && !stuck)
+          stuck = !__all_sync(0xffffffffu, mbar_wait(&sh->item_empty[n & 1], ((n >> 1) - 1) & 1, kListWait));
+        if (stuck) {  // nobody takes these any more; the merge still needs the rows' places
+          if (it.index < 0) break;
+          if (lane == 0) atomicOr(&p.status[it.b], kSeqTimeout);
+          continue;
+        }
         if (lane == 0) {
           sh->item[n & 1] = it;
           mbar_arrive(&sh->item_full[n & 1]);
@@ -864,12 +948,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (dual || pipe == 0) {
-      const bool whole = g.nr == 1;
+      const bool whole = g.whole;
       const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
       w0 *= inv;
       w1 *= inv;
       uint8_t* stage = q_s + pipe * kQTile;  // of a pair: this pipe's query tile, [128 rows][2 D bytes], chunks rotated
-      const int64_t rec = 2 * (int64_t)g.index + pipe;
+      const int64_t rec = g.rec + pipe;
       float4* dst = reinterpret_cast<float4*>(p.ws_o) + rec * (D / 4) * p.rec_rows;
       uint4* out_row = reinterpret_cast<uint4*>(p.out + query_row(p, b, hk, min(gr, p.rows - 1)) * D);
 #pragma unroll 1
@@ -940,33 +1024,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < p.B; ++b) atomicOr(&p.status[b], kSeqTimeout);
 }
 
-// Joins the records of sequences whose key range was split: out = sum_i 2^(m_i -
-// m) O_i / sum_i 2^(m_i - m) l_i.  One thread per row and four columns.
+// Joins the records of the rows that were cut: out = sum_i 2^(m_i - m) O_i / sum_i
+// 2^(m_i - m) l_i.  Block x: a query tile of a (sequence, kv head); one thread per
+// row and four columns.
 template <int D>
 __global__ void __launch_bounds__(256) scored_merge_kernel(const __grid_constant__ ScoredParams p) {
-  __shared__ int red[8];
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int len = __ldcg(p.plan);
-  const float4* ws_o = reinterpret_cast<const float4*>(p.ws_o);
+  const int tid = threadIdx.x;
   const int qt = blockIdx.x % p.nqt, hk = blockIdx.x / p.nqt % p.Hkv, b = blockIdx.x / p.nqt / p.Hkv;
-  const int nr = ranges_of(sequence(p, b).nt, len);
-  if (nr == 1) return;
-  int before = 0;
-  for (int i = threadIdx.x; i < b; i += 256) before += ranges_of(sequence(p, i).nt, len);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = before;
-  __syncthreads();
-  before = 0;
-  for (int i = 0; i < 8; ++i) before += red[i];
+  const int2 ctas = __ldcg(p.ws_row + ((int64_t)b * p.Hkv + hk) * p.npairs + qt / 2);
+  if (ctas.x < 0) return;
+  const int nr = ctas.y - ctas.x + 1;
+  // the pieces lie in CTAs one after another, the first at its end, the others at their starts
+  auto record = [&](int i) -> int64_t { return 2 * (2 * (ctas.x + i) + (i == 0)) + (qt & 1); };
   const int rows = min(kQRows, p.rows - qt * kQRows);
-  const int64_t item0 = ((int64_t)before * p.Hkv + (int64_t)hk * nr) * p.npairs + qt / 2;
-  const int pipe = qt & 1;
   const bool fail = p.status[b] != 0;
-  for (int e = blockIdx.y * 256 + threadIdx.x; e < rows * (D / 4); e += gridDim.y * 256) {
+  const float4* ws_o = reinterpret_cast<const float4*>(p.ws_o);
+  for (int e = blockIdx.y * 256 + tid; e < rows * (D / 4); e += gridDim.y * 256) {
     const int r = e % rows, c = e / rows;
-    float m = -INFINITY, l = 0.f;
+    float mx = -INFINITY, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int U = 8;  // records in flight
     for (int i0 = 0; i0 < nr; i0 += U) {
@@ -977,16 +1054,16 @@ __global__ void __launch_bounds__(256) scored_merge_kernel(const __grid_constant
         ml[i] = make_float2(-INFINITY, 0.f);
         o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i0 + i < nr) {
-          const int64_t rec = 2 * (item0 + (int64_t)(i0 + i) * p.npairs) + pipe;
+          const int64_t rec = record(i0 + i);
           ml[i] = __ldcg(p.ws_ml + rec * p.rec_rows + r);
           o[i] = __ldcg(ws_o + (rec * (D / 4) + c) * p.rec_rows + r);
         }
       }
-      float mm = m;
+      float mm = mx;
 #pragma unroll
       for (int i = 0; i < U; ++i) mm = fmaxf(mm, ml[i].x);
       const float ms = mm == -INFINITY ? 0.f : mm;
-      const float w = fast_exp2(m - ms);
+      const float w = fast_exp2(mx - ms);
       l *= w;
       a = make_float4(a.x * w, a.y * w, a.z * w, a.w * w);
 #pragma unroll
@@ -995,14 +1072,14 @@ __global__ void __launch_bounds__(256) scored_merge_kernel(const __grid_constant
         l = fmaf(wi, ml[i].y, l);
         a = make_float4(fmaf(wi, o[i].x, a.x), fmaf(wi, o[i].y, a.y), fmaf(wi, o[i].z, a.z), fmaf(wi, o[i].w, a.w));
       }
-      m = mm;
+      mx = mm;
     }
     const float inv = !fail && l > 0.f ? 1.f / l : 0.f;
     uint2 v = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
     if (fail) v = make_uint2(0u, 0u);
     *reinterpret_cast<uint2*>(p.out + query_row(p, b, hk, qt * kQRows + r) * D + 4 * c) = v;
   }
-  }
+}
 
 // [BH][S_cap][D] bf16 in boxes of kKeys rows: 64 columns (D = 64), or both 64-column
 // halves of a row (D = 128), landing as [half][row][128 B], 128-byte swizzle.
@@ -1028,30 +1105,29 @@ bool encode_scored_map(CUtensorMap* map, const void* base, int64_t BH, int64_t S
 
 // Grid and workspace of a shape (lengths are known on the device only).
 struct ScoredPlan {
-  int64_t grid, max_items;
-  int sms, nqt, npairs, split, cand_step, rec_rows;
-  size_t ml_off, ws_bytes;  // plan word, records, (reference, sum) pairs
+  int grid, nqt, npairs, merge, rec_rows;
+  size_t ml_off, row_off, ws_bytes;  // records, (reference, sum) pairs, rows' CTAs
 };
 
 tv_status plan_scored(int B, int M, int Hq, int Hkv, int D, int64_t S_cap, int window, ScoredPlan& lp) {
-  const tv_status r = current_sms(lp.sms);
+  const tv_status r = current_sms(lp.grid);
   if (r != TV_OK) return r;
   const int rows = (Hq / Hkv) * (M + 1);
   lp.nqt = (rows + kQRows - 1) / kQRows;
   lp.npairs = (lp.nqt + 1) / 2;
   lp.rec_rows = std::min(kQRows, rows);
-  const int64_t base = (int64_t)B * Hkv * lp.npairs;
   int64_t keys = std::max<int64_t>(S_cap, 1);
   if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window - 1 + M + 1);
+  // shorter rows are never cut
   const int64_t tiles = (keys + kKeys - 1) / kKeys;
-  // Ranges are split while the sequences give fewer than kMaxRounds items per SM.
-  lp.split = base < kMaxRounds * (int64_t)lp.sms && tiles >= 2 * kMinSplitTiles && tiles < (1 << 20);
-  lp.max_items = lp.split ? kMaxRounds * (int64_t)lp.sms : base;
-  lp.grid = std::min<int64_t>(lp.max_items, lp.sms);
-  lp.cand_step = (int)((tiles + kThreads - kMinSplitTiles - 2) / (kThreads - kMinSplitTiles - 1));
-  const size_t recs = lp.split ? 2 * (size_t)lp.max_items * lp.rec_rows : 0;
-  lp.ml_off = 256 + recs * D * sizeof(float);
-  lp.ws_bytes = lp.split ? lp.ml_off + recs * sizeof(float2) : 0;
+  lp.merge = tiles >= 2 * kMinTiles;
+  // the dealing counts rows of work, and their cost, in 31 bits
+  if (std::max<int64_t>(tiles, lp.grid) * Hkv > 0x3fffffffLL || (double)tiles * Hkv * B * lp.nqt > 1e9)
+    return TV_ERR_UNSUPPORTED;
+  const size_t recs = lp.merge ? 4 * (size_t)lp.grid * lp.rec_rows : 0;
+  lp.ml_off = recs * D * sizeof(float);
+  lp.row_off = lp.ml_off + recs * sizeof(float2);
+  lp.ws_bytes = lp.merge ? lp.row_off + (size_t)B * Hkv * lp.npairs * sizeof(int2) : 0;
   return TV_OK;
 }
 
@@ -1066,12 +1142,12 @@ tv_status launch_scored(int mode, const CUtensorMap& tmk, const CUtensorMap& tmv
   const size_t smem = 2 * (D / 64) * kQHalf + kRingBytes + sizeof(Shared);
   tv_status r = allow_shared(reinterpret_cast<const void*>(kern), (int)smem);
   if (r != TV_OK) return r;
-  r = launch(kern, dim3((unsigned)lp.grid), dim3(kThreads), smem, s, 1, true, tmk, tmv, p);
-  if (r != TV_OK || !lp.split) return r;
-  // about four blocks an SM (at most 16 have work per unit): most find a sequence in one range and leave
-  const int units = p.B * p.Hkv * p.nqt;
-  const int parts = std::max(1, std::min((lp.rec_rows * (D / 4) + 255) / 256, 4 * lp.sms / units));
-  return launch(scored_merge_kernel<D>, dim3(units, parts), dim3(256), 0, s, 1, true, p);
+  const int64_t units = (int64_t)p.B * p.Hkv * p.nqt;
+  r = launch(kern, dim3((unsigned)p.grid), dim3(kThreads), smem, s, 1, true, tmk, tmv, p);
+  if (r != TV_OK || !lp.merge) return r;
+  // about four blocks an SM (at most 16 have work per unit): most find a row whole and leave
+  const int parts = std::max(1, (int)std::min<int64_t>((lp.rec_rows * (D / 4) + 255) / 256, 4 * lp.grid / units));
+  return launch(scored_merge_kernel<D>, dim3((unsigned)units, parts), dim3(256), 0, s, 1, true, p);
 }
 
 }  // namespace
@@ -1109,7 +1185,7 @@ extern "C" tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k,
   ScoredPlan lp;
   tv_status r = plan_scored(B, M, Hq, Hkv, D, S_cap, window, lp);
   if (r != TV_OK) return r;
-  if (lp.max_items > 0x3fffffffLL || (int64_t)B * Hkv * lp.nqt > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
+  if ((int64_t)B * Hkv * lp.nqt > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
   if (lp.ws_bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < lp.ws_bytes))
     return TV_ERR_INVALID_ARG;
   ScoredParams p = {};
@@ -1136,9 +1212,8 @@ extern "C" tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k,
   p.nqt = lp.nqt;
   p.npairs = lp.npairs;
   p.rec_rows = lp.rec_rows;
-  p.max_items = lp.max_items;
-  p.split = lp.split;
-  p.cand_step = lp.cand_step;
+  // rows that are never cut want no more CTAs than there are rows
+  p.grid = lp.merge ? lp.grid : (int)std::min<int64_t>(lp.grid, (int64_t)B * Hkv * lp.npairs);
   const double log2e = 1.4426950408889634;
   p.scale_log2 = (float)(scale * log2e);
   int mode = alibi_slopes ? kBias : kPlain;
@@ -1154,10 +1229,10 @@ extern "C" tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k,
     p.ref = (float)std::min(cap2, 110.0 - cap2);
   }
   p.wait_limit_ns = pipeline_wait_limit_ns();
-  if (lp.split) {
-    p.plan = static_cast<int*>(workspace);
-    p.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
+  if (lp.merge) {
+    p.ws_o = static_cast<float*>(workspace);
     p.ws_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + lp.ml_off);
+    p.ws_row = reinterpret_cast<int2*>(static_cast<char*>(workspace) + lp.row_off);
   }
   CUtensorMap tmk, tmv;
   const int64_t BH = (int64_t)p.n_slots * Hkv;
