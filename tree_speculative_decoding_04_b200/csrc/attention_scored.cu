@@ -32,8 +32,11 @@
 // keys leave P columns of its own beside S, so the next S is formed while the
 // softmax still works on this one.  (Tiles of 128 keys with P written over S: PV
 // and the next QK lay between two softmax phases of a pipe, 1.0 us after 1.1-1.4
-// us of softmax; 128 query rows x 64 heads x 8 sequences of 4096-16384 keys took
-// 551 us.)
+// us of softmax; 129 query rows x 64 heads x 8 sequences of 4096-16384 keys took
+// 551 us, and 530 us with tiles of 80 keys, both with equal ranges dealt in turn.)
+// What bounds it: the softmax warps, two to a scheduler, 1.3-1.45 us per pair of tiles
+// (MUFU 45-57 %, tensor pipe 45-54 %).  Four to a scheduler, each with half of a row's
+// columns, took 616 us: twice the TMEM accesses at half the width.
 #include <algorithm>
 #include <climits>
 
@@ -58,7 +61,7 @@ constexpr int kColP = kKeys, kColO = 128;
 constexpr float kGrow = 24.0f;
 constexpr int kMaxBatch = 4096;
 constexpr int kMinTiles = 6;               // no cut nearer to a row's ends than this many key tiles
-constexpr int kSecondItem = 6;             // what a CTA's second item costs on top, in key tiles
+constexpr int kSecondItem = 14;            // what a CTA's second item costs on top, in key tiles of a lone query tile
 
 // Which scores an instance computes.
 //   kCapLow: capped with cap * log2e <= kLowCap: every exponent lies within that of
@@ -122,10 +125,16 @@ __device__ __forceinline__ Geo sequence(const ScoredParams& p, int b) {
 //            tile takes half the time), and every CTA takes the same cost
 //   by piece (per > 0) a row makes equal pieces of at most `per` key tiles, and every
 //            CTA takes one piece
-// A share by cost crosses from row to row, and every further item costs the filling and
-// draining of the pipes and an epilogue; pieces are uneven.  So: pieces where there is a
-// CTA for every row and the longest piece is no longer than an even share and kSecondItem
-// tiles, and cost elsewhere.
+// A share by cost crosses from row to row, and every further item costs its queries' way
+// into shared memory (2-3 us), the filling and draining of the pipes (2 us) and an
+// epilogue (1.3-2.5 us); pieces are uneven.  So: pieces where there is a CTA for every
+// row and the longest piece costs no more than an even share and kSecondItem, and shares
+// by cost elsewhere.  Measured by piece / by cost, with the longest piece and the even
+// share in key tiles: window of 4096 keys, 8 kv heads, 11 sequences (52, 31) 54.3 / 50.2
+// us, 14 sequences (52, 39) 55.6 / 57.2 us, 8 sequences (26, 22) 37.5 / 42.3 us; biases, 3
+// query tiles, 8 sequences (52, 33) 59.0 / 54.4 us.  Equal ranges of every sequence dealt
+// in turn took 172 us for 32 sequences with biases that take 137 us so, and 563 us for
+// 129 query rows x 64 heads x 8 sequences that take 510 us.
 __device__ __forceinline__ int tiles_of(int nt) { return max(nt, 1); }  // (a sequence without keys has rows to zero)
 
 struct Shares {  // (the host has checked that all of it fits in 31 bits)
@@ -180,7 +189,7 @@ struct Shared {
   int failed;
   Item item[2];
   float2 join_ml[kQRows];
-  uint8_t depth[kMaxRows];
+  float depth[kMaxRows];
   uint32_t anc[2 * kQRows][kMaxRows / 32 + 1];  // ancestor words of the softmax threads' rows
 };
 constexpr int kItemReaders = 3 + 8;  // the producer warp, both MMA threads, the softmax warps
@@ -204,18 +213,14 @@ __device__ __forceinline__ float cap_score(float x, const ScoredParams& p) {
 }
 
 // 16 scores of a row, minus `sub`, from the raw products x of keys kc .. kc+15, in
-// the general form.  ok: the keys that count (used where `edge`; what lies behind
-// the step's rows may be anything).  slope2, pos: the row's bias per position
+// the general form.  ok: the keys that count (used where `edge`; what the others
+// hold may be anything, and is replaced at the end).  slope2, pos: the row's bias per position
 // (log2) and its position; dep: the tree rows' depths.
 template <int MODE>
 __device__ __forceinline__ void chunk_scores(float (&x)[16], const ScoredParams& p, bool edge, uint32_t ok, float sub,
-                                             float slope2, int pos, int kc, int kl, int du, const uint8_t* dep) {
+                                             float slope2, int pos, int kc, int kl, int M, const float* dep) {
   constexpr bool CAP = MODE == kCapLow || MODE == kCapHigh || MODE == kCapBias;
   constexpr bool BIAS = MODE == kBias || MODE == kCapBias;
-  if (edge) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = (ok >> j) & 1u ? x[j] : 0.f;
-  }
   bool far = false;
   if (CAP) {
     float a[2] = {fabsf(x[0]), fabsf(x[1])};
@@ -244,8 +249,8 @@ __device__ __forceinline__ void chunk_scores(float (&x)[16], const ScoredParams&
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const int t = kc + j - kl;  // tree row
-      const int dist = t < 0 ? pos - (kc + j) : du - (int)dep[min(t, p.M)];
-      x[j] += fmaf(-slope2, (float)dist, -sub);
+      const float off = t < 0 ? (float)t : dep[min(t, M)];  // the key's position less kl
+      x[j] += fmaf(slope2, off - (float)(pos - kl), -sub);
     }
   } else {
 #pragma unroll
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           units = __shfl_sync(0xffffffffu, n, __ffs(m) - 1);
         }
         const int full = p.nqt > 1 ? 2 : 1;
-        if ((int64_t)full * (min(per, longest) - kSecondItem) * p.grid > tiles * p.Hkv * p.nqt) {
+        if (((int64_t)full * min(per, longest) - kSecondItem) * p.grid > tiles * p.Hkv * p.nqt) {
           per = 0;
           units = tiles;
         }
@@ -495,6 +500,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (it.index < 0) break;
+        if (it.nt > 0) {  // the query rows on their way to L2 while the item before is at work
+          const int rows = min(it.dual ? 2 * kQRows : kQRows, p.rows - it.qt0 * kQRows);
+          for (int e = lane; e < rows * kHalves; e += 32)
+            prefetch_l2(p.q + query_row(p, it.b, it.hk, it.qt0 * kQRows + e / kHalves) * D + e % kHalves * 64);
+        }
       }
     } else if (warp == 0) {
       // -------------------------------------------------------------- K and V stream
@@ -512,6 +522,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t s = idx % kSlots;
           if (idx >= (uint32_t)kSlots &&
               !__all_sync(0xffffffffu, mbar_wait(&sh->empty[s], ((idx / kSlots) - 1) & 1, lim))) {
+            failed = true;
+            break;
+          }
+          // The first query tiles come before the ring's fill: every CTA starts with
+          // both, and the products wait for the queries.
+          if (idx == 2 && kj + vj == 2 && !__all_sync(0xffffffffu, mbar_wait(&sh->q_full, 0, lim))) {
             failed = true;
             break;
           }
@@ -652,13 +668,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (int i = 0; i < kW; ++i) sh->anc[stid][i] = a[i];
-      if (stid <= p.M) sh->depth[stid] = (uint8_t)d;
+      if (stid <= p.M) sh->depth[stid] = (float)d;
       fence_async_smem();
       tc_fence_before();
       asm volatile("bar.sync 3, 256;" ::: "memory");
       if (lane == 0) mbar_arrive(&sh->q_full);
     }
-    const int du = (p.window > 0 || BIAS) && nt > 0 ? sh->depth[u] : 0;
+    const int du = (p.window > 0 || BIAS) && nt > 0 ? (int)sh->depth[u] : 0;
     const float slope2 =
         BIAS ? __ldg(p.slopes + hk * p.G + (row_ok ? gr - u * p.G : 0)) * 1.4426950408889634f : 0.f;
     const int pos = g.kl + du;
@@ -801,26 +817,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return w;
           };
-          if (!wait_pv()) {
-            to = true;
-            break;
-          }
-          if (TRACK) {
+          // scores of keys kc .. kc+15 less `sub`
+          auto scores = [&](int c, float sub, float (&x)[16]) {
+            uint32_t raw[16];
+            tmem_ld16(t_s + c * 16, raw);
+            const uint32_t ok = edge ? allowed(key0 + 16 * c) : ~0u;
+            tmem_wait_ld16(raw);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(raw[e]);
+            chunk_scores<MODE>(x, p, edge, ok, sub, slope2, pos, key0 + 16 * c, g.kl, p.M, sh->depth);
+          };
+          if (TRACK) {  // first the maximum; the scores wait in S's place
             float mx = -INFINITY;
 #pragma unroll 1
             for (int c = 0; c < kKeys / 16; ++c) {
-              uint32_t raw[16];
-              tmem_ld16(t_s + c * 16, raw);
-              const uint32_t ok = edge ? allowed(key0 + 16 * c) : ~0u;
-              tmem_wait_ld16(raw);
               float x[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(raw[e]);
-              chunk_scores<MODE>(x, p, edge, ok, 0.f, slope2, pos, key0 + 16 * c, g.kl, du, sh->depth);
+              scores(c, 0.f, x);
               float a[2] = {fmaxf(mx, x[0]), x[1]};
 #pragma unroll
               for (int e = 2; e < 16; e += 2) a[(e >> 1) & 1] = fmax3(a[(e >> 1) & 1], x[e], x[e + 1]);
               mx = fmaxf(a[0], a[1]);
+              uint32_t back[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) back[e] = __float_as_uint(x[e]);
+              tmem_st16(t_s + c * 16, back);
+            }
+            tmem_wait_st();
+            if (!wait_pv()) {
+              to = true;
+              break;
             }
             // The reference follows the maximum lazily: O is rescaled (a TMEM access of
             // the whole warp, each row by its own factor) only when some row's maximum
@@ -845,18 +870,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               l2[0] = l2[1] = 0ull;
             }
             if (grow) m = mx;
+          } else if (!wait_pv()) {
+            to = true;
+            break;
           }
           const float sub = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
           for (int c = 0; c < kKeys / 16; ++c) {
-            uint32_t raw[16];
-            tmem_ld16(t_s + c * 16, raw);
-            const uint32_t ok = edge ? allowed(key0 + 16 * c) : ~0u;
-            tmem_wait_ld16(raw);
             float x[16];
+            if (TRACK) {
+              uint32_t raw[16];
+              tmem_ld16(t_s + c * 16, raw);
+              tmem_wait_ld16(raw);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(raw[e]);
-            chunk_scores<MODE>(x, p, edge, ok, sub, slope2, pos, key0 + 16 * c, g.kl, du, sh->depth);
+              for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(raw[e]) - sub;
+            } else {
+              scores(c, sub, x);
+            }
             uint32_t pk[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
