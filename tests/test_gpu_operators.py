@@ -243,6 +243,24 @@ def test_attention_scored_large_batch_and_trees():
         _check_attn(out, q, k, v, ks, kl, par, softcap=50.0)
 
 
+@pytest.mark.parametrize("B,M,Hq,Hkv,D,lens,failed", [
+    (3, 0, 8, 1, 128, [6000, 1, 2500], ()),                     # pieces of rows of very different lengths
+    (9, 3, 32, 8, 64, [4000, 0, 977, 955, 2880, 1, 79, 80, 3999], (4,)),   # pieces or shares; an invalid row between
+    (50, 1, 16, 4, 64, [1000 + 37 * i % 900 for i in range(50)], (0, 49)),  # more rows than CTAs, one query tile
+    (30, 23, 64, 4, 128, [(i * 331) % 1500 for i in range(30)], (7,)),      # three query tiles: pairs and lone ones
+    (40, 16, 20, 1, 64, [0] * 20 + [2400] + [5] * 19, ()),     # one long row among rows of one tile
+    (300, 2, 2, 1, 64, [i % 3 * 40 for i in range(300)], (5,)),             # rows too short to cut
+])
+def test_attention_scored_rows_cut_between_ctas(B, M, Hq, Hkv, D, lens, failed):
+    q, k, v, ks, kl, par = _attn_case(B, M, Hq, Hkv, D, lens, 5 + B)
+    status = [4 if b in failed else 0 for b in range(B)]
+    for kw in (dict(softcap=30.0), dict(slopes=_slopes(Hq)), dict(window=1100)):
+        out, _ = _attend(q, k, v, ks, kl, par, status_override=status, **kw)
+        _check_attn(out, q, k, v, ks, kl, par, status=status, **kw)
+        again, _ = _attend(q, k, v, ks, kl, par, status_override=status, **kw)
+        assert torch.equal(out, again)
+
+
 def test_attention_scored_repeats_exactly_and_on_another_stream():
     q, k, v, ks, kl, par = _attn_case(2, 16, 8, 2, 128, [4000, 2500], 21)
     a, _ = _attend(q, k, v, ks, kl, par, softcap=50.0)

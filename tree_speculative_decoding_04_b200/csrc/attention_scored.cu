@@ -101,8 +101,8 @@ struct ScoredParams {
 
 // A sequence's place in the cache, the first key that its root sees and the key
 // tiles from there (0: bad slot or geometry).  Its status has no part in this:
-// a call's CTAs and its merge form the plan at different times, and a sequence
-// may fail in between.
+// a call's CTAs form the plan at different times, and a sequence may fail in
+// between.
 struct Geo {
   int sl, ks, kl, first, nt;
 };
@@ -1140,8 +1140,6 @@ struct ScoredPlan {
 };
 
 tv_status plan_scored(int B, int M, int Hq, int Hkv, int D, int64_t S_cap, int window, ScoredPlan& lp) {
-  const tv_status r = current_sms(lp.grid);
-  if (r != TV_OK) return r;
   const int rows = (Hq / Hkv) * (M + 1);
   lp.nqt = (rows + kQRows - 1) / kQRows;
   lp.npairs = (lp.nqt + 1) / 2;
@@ -1150,10 +1148,11 @@ tv_status plan_scored(int B, int M, int Hq, int Hkv, int D, int64_t S_cap, int w
   if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window - 1 + M + 1);
   // shorter rows are never cut
   const int64_t tiles = (keys + kKeys - 1) / kKeys;
+  // the dealing counts the key tiles of all rows of work in 31 bits
+  if ((double)tiles * Hkv * B * lp.nqt > (double)(1 << 30)) return TV_ERR_UNSUPPORTED;
+  const tv_status r = current_sms(lp.grid);
+  if (r != TV_OK) return r;
   lp.merge = tiles >= 2 * kMinTiles;
-  // the dealing counts rows of work, and their cost, in 31 bits
-  if (std::max<int64_t>(tiles, lp.grid) * Hkv > 0x3fffffffLL || (double)tiles * Hkv * B * lp.nqt > 1e9)
-    return TV_ERR_UNSUPPORTED;
   const size_t recs = lp.merge ? 4 * (size_t)lp.grid * lp.rec_rows : 0;
   lp.ml_off = recs * D * sizeof(float);
   lp.row_off = lp.ml_off + recs * sizeof(float2);
@@ -1175,8 +1174,9 @@ tv_status launch_scored(int mode, const CUtensorMap& tmk, const CUtensorMap& tmv
   const int64_t units = (int64_t)p.B * p.Hkv * p.nqt;
   r = launch(kern, dim3((unsigned)p.grid), dim3(kThreads), smem, s, 1, true, tmk, tmv, p);
   if (r != TV_OK || !lp.merge) return r;
-  // about four blocks an SM (at most 16 have work per unit): most find a row whole and leave
-  const int parts = std::max(1, (int)std::min<int64_t>((lp.rec_rows * (D / 4) + 255) / 256, 4 * lp.grid / units));
+  // About eight blocks an SM, and at least one for each query tile: a block whose tile has
+  // no pieces leaves at once.
+  const int parts = std::max(1, (int)std::min<int64_t>((lp.rec_rows * (D / 4) + 255) / 256, 8 * lp.grid / units));
   return launch(scored_merge_kernel<D>, dim3((unsigned)units, parts), dim3(256), 0, s, 1, true, p);
 }
 
@@ -1215,7 +1215,6 @@ extern "C" tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k,
   ScoredPlan lp;
   tv_status r = plan_scored(B, M, Hq, Hkv, D, S_cap, window, lp);
   if (r != TV_OK) return r;
-  if ((int64_t)B * Hkv * lp.nqt > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
   if (lp.ws_bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < lp.ws_bytes))
     return TV_ERR_INVALID_ARG;
   ScoredParams p = {};
