@@ -228,7 +228,7 @@ tv_status tree_attention_noalloc(const uint16_t* q, const uint16_t* k, const uin
  * finite values; prefix columns before the root's window are not used, whatever
  * they hold.
  * TV_ERR_UNSUPPORTED: B > 4096, (Hq / Hkv) * (M + 1) >= 2^21, scale > 10^4 softcap,
- * more than 2^30 tiles: B * Hkv * ceil((Hq / Hkv) (M + 1) / 128) * ceil(K / 80) with
+ * more than 2^30 tiles: B * Hkv * ceil((Hq / Hkv) (M + 1) / 128) * ceil(K / 64) with
  * K = S_cap or, if less, window + M.
  * The softmax weights are rounded to bf16 before their product with V; scores,
  * sums and the merge of split key ranges are fp32.

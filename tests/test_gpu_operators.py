@@ -245,6 +245,9 @@ def test_attention_scored_large_batch_and_trees():
 
 @pytest.mark.parametrize("B,M,Hq,Hkv,D,lens,failed", [
     (3, 0, 8, 1, 128, [6000, 1, 2500], ()),                     # pieces of rows of very different lengths
+    (5, 7, 8, 2, 64, [3000, 64, 65, 127, 800], (2,)),            # few rows: 32, and keys that end inside a chunk
+    (2, 32, 2, 2, 128, [5000, 4100], ()),                        # one row more than few
+    (120, 0, 12, 1, 128, [i * 13 % 1300 for i in range(120)], (3,)),        # few rows, shares by cost
     (9, 3, 32, 8, 64, [4000, 0, 977, 955, 2880, 1, 79, 80, 3999], (4,)),   # pieces or shares; an invalid row between
     (50, 1, 16, 4, 64, [1000 + 37 * i % 900 for i in range(50)], (0, 49)),  # more rows than CTAs, one query tile
     (30, 23, 64, 4, 128, [(i * 331) % 1500 for i in range(30)], (7,)),      # three query tiles: pairs and lone ones
@@ -595,7 +598,8 @@ def test_attention_scored_wait_limit():
     assert torch.equal(again, ref) and int(status.abs().sum()) == 0
 
 
-@pytest.mark.parametrize("M,Hq,lens", [(0, 32, [3431, 583, 935, 3652, 609, 1846, 579, 3760]), (16, 64, [3000, 1500, 700]),
+@pytest.mark.parametrize("M,Hq,lens", [(0, 32, [3431, 583, 935, 3652, 609, 1846, 579, 3760]),
+                                       (0, 32, [1431, 583, 935, 1652, 609, 1846, 579, 760]), (16, 64, [3000, 1500, 700]),
                                        (40, 16, [2500, 90])])
 def test_attention_scored_thousands_of_launches(M, Hq, lens):
     """Lone and paired query tiles over split ranges, queued thousands deep: one answer, no sequence flagged.  (The

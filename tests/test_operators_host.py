@@ -55,7 +55,7 @@ def _attn(lib, **kw):
     (dict(window=-1), INVALID), (dict(window=4, depth=z), INVALID), (dict(slopes=d, depth=z), INVALID),
     (dict(D=96), UNSUPPORTED), (dict(M=256), UNSUPPORTED), (dict(S=2 ** 31), UNSUPPORTED), (dict(q=P(264)), INVALID),
     (dict(out=z), INVALID), (dict(slot=d), INVALID), (dict(status=z), INVALID), (dict(B=0, q=z), 0),
-    (dict(B=4096, M=255, Hq=4096, Hkv=1, S=2 ** 20), UNSUPPORTED),  # 2^12 * 2^13 * 2^13.7 tiles
+    (dict(B=4096, M=255, Hq=4096, Hkv=1, S=2 ** 20), UNSUPPORTED),  # 2^12 * 2^13 * 2^14 tiles
 ])
 def test_attention_refusals(lib, kw, rc):
     assert _attn(lib, **kw) == rc

@@ -34,6 +34,8 @@
 // and the next QK lay between two softmax phases of a pipe, 1.0 us after 1.1-1.4
 // us of softmax; 129 query rows x 64 heads x 8 sequences of 4096-16384 keys took
 // 551 us, and 530 us with tiles of 80 keys, both with equal ranges dealt in turn.)
+// With few query rows a tile has 64 keys and its softmax is shared by a pipe's four
+// warps (kFewRows).
 // What bounds it: the softmax warps, two to a scheduler, 1.3-1.45 us per pair of tiles
 // (MUFU 45-57 %, tensor pipe 45-54 %).  Four to a scheduler, each with half of a row's
 // columns, took 616 us: twice the TMEM accesses at half the width.
@@ -47,14 +49,21 @@ namespace tv {
 namespace {
 
 constexpr int kQRows = 128;
-constexpr int kKeys = 80;                  // keys per tile
-constexpr int kHalf = kKeys * 128;         // one 64-column half of a K or V tile: 80 rows x 128 B
+// The few-row form: up to 32 query rows per kv head, and few keys.  All four softmax
+// warps of a pipe get the same rows, and each forms the weights of 16 of the 64 keys of a
+// tile, so a tile's softmax takes 0.5 us instead of 1.0-1.4.  Longer ranges stream their
+// keys at the rate of HBM either way, and there the wider tiles are the better ones.
+// Few-row / general form, 8 kv heads of 4 query heads, by keys per SM: 8 sequences of up to
+// 4096 keys, single tokens (1770) 28.0 / 28.2 us, 16 of 4096 (3540) 58.3 / 53.5 us; 6 rows
+// and a window of 4096, 8 sequences (1770) 37.4 / 36.6 us, 5 (1110) 27.9 / 29.1 us,
+// 2 (440) 17.3 / 20.5 us; one sequence of 4096 keys (220) 13.5 / 17.2 us.
+constexpr int kFewRows = 32, kFewKeys = 1500;  // query rows; keys per SM
+constexpr int keys_of(bool few) { return few ? 64 : 80; }  // keys per tile
 constexpr int kQHalf = kQRows * 128;       // of a query tile
-constexpr int kRingBytes = 14 * kHalf;
+constexpr int kRingBytes = 140 * 1024;
 constexpr int kMaxSlots = 14;
 constexpr int kThreads = 384;
-// TMEM columns of a pipe's 256
-constexpr int kColP = kKeys, kColO = 128;
+constexpr int kColO = 128;                 // TMEM column of O in a pipe's 256
 // A row's reference moves once a score lies more than 2^kGrow above it (the
 // weights are floats in bf16 and sums in fp32: a large weight is as exact as a
 // small one, and 2^24 leaves both far from their limits).
@@ -107,6 +116,7 @@ struct Geo {
   int sl, ks, kl, first, nt;
 };
 
+template <int KEYS>
 __device__ __forceinline__ Geo sequence(const ScoredParams& p, int b) {
   Geo g{cache_slot(p.slot, b, p.n_slots), 0, 0, 0, 0};
   if (g.sl < 0) return g;
@@ -114,7 +124,7 @@ __device__ __forceinline__ Geo sequence(const ScoredParams& p, int b) {
   g.kl = __ldcg(p.kv_len + g.sl);
   if (!geometry_ok(g.ks, g.kl, p.M, p.S_cap)) return g;
   if (p.window > 0) g.first = max(0, g.kl - (p.window - 1));
-  g.nt = (g.kl - g.first + p.M + 1 + kKeys - 1) / kKeys;
+  g.nt = (g.kl - g.first + p.M + 1 + KEYS - 1) / KEYS;
   return g;
 }
 
@@ -262,7 +272,7 @@ __device__ __forceinline__ void chunk_scores(float (&x)[16], const ScoredParams&
   }
 }
 
-template <int D, int MODE>
+template <int D, int MODE, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
     scored_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const __grid_constant__ ScoredParams p) {
@@ -270,10 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool CAP = MODE == kCapLow || MODE == kCapHigh || MODE == kCapBias;
   constexpr bool TRACK = MODE != kCapLow;  // a running maximum is kept
   constexpr int kHalves = D / 64;
+  constexpr int kKeys = keys_of(FEW), kColP = kKeys;
+  constexpr int kHalf = kKeys * 128;       // one 64-column half of a K or V tile: rows of 128 B
+  constexpr int kChunks = FEW ? 1 : kKeys / 16;  // 16-key chunks that a softmax warp works on
   constexpr int kTile = kHalves * kHalf;   // K or V tile
   constexpr int kQTile = kHalves * kQHalf;
-  constexpr int kSlots = kRingBytes / kTile;
-  static_assert(kSlots <= kMaxSlots, "ring");
+  constexpr int kSlots = kRingBytes / kTile < kMaxSlots ? kRingBytes / kTile : kMaxSlots;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* q_s = smem;                // [2][halves][128][128 B]
   uint8_t* ring = smem + 2 * kQTile;  // [slots][halves][80][128 B]
@@ -315,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int4* geo_s = reinterpret_cast<int4*>(ring + 4 * kMaxBatch);
   for (int b = tid; b < p.B; b += kThreads) {
     const int st = __ldcg(p.status + b);
-    const Geo g = sequence(p, b);
+    const Geo g = sequence<kKeys>(p, b);
     nt_s[b] = g.nt;
     geo_s[b] = make_int4(g.sl, g.ks, g.kl, st);
   }
@@ -338,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (at.b < p.B && at.before * p.Hkv * shares.head < at.hi) {
       if (at.fresh) {
         at.st = __ldcg(p.status + at.b);
-        at.g = sequence(p, at.b);
+        at.g = sequence<kKeys>(p, at.b);
         at.n = shares.units_of(tiles_of(at.g.nt));
         at.fresh = false;
       }
@@ -627,30 +639,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pipe = (warp - 4) >> 2;
     const int r = (warp & 3) * 32 + lane;
     const int stid = tid - 128;  // of the 256 softmax threads
-    const uint32_t t_s = tmem + pipe * 256 + ((uint32_t)((warp & 3) * 32) << 16), t_p = t_s + kColP, t_o = t_s + kColO;
+    const uint32_t t_row = tmem + pipe * 256 + ((uint32_t)((warp & 3) * 32) << 16), t_o = t_row + kColO;
+    const uint32_t t_s = t_row + (FEW ? (warp & 3) * 16 : 0), t_p = t_row + kColP + (FEW ? (warp & 3) * 8 : 0);
+    if (FEW) {  // the other warps' keys have no weight in this warp's rows
+      uint32_t z[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) z[e] = 0u;
+      tmem_st32(t_row + kColP, z);
+      tmem_wait_st();
+    }
     uint32_t base = 0, step0 = 0;  // ring entries and steps of earlier items
     bool to = false;  // a wait ran out: zero rows from here on
     for (int n_item = 0;; ++n_item) {
     const Item g = next_item(n_item);
     if (g.index < 0) break;
-    const bool dual = g.dual;
+    const bool dual = !FEW && g.dual;
     const int nt = g.nt, hk = g.hk, b = g.b;
     const int qt = dual ? g.qt0 + pipe : g.qt0;
-    const int gr = qt * kQRows + r;
+    const int gr = FEW ? lane : qt * kQRows + r;
     const bool row_ok = gr < p.rows;
     const bool warp_live = __any_sync(0xffffffffu, row_ok);
     const int u = min(node_of(p, min(gr, p.rows - 1)), p.M);
     if (nt > 0) {  // query rows -> swizzled shared memory; the tree rows' depths
       // A thread brings one 16-byte column of every 16th (D = 128) or 32nd row, all
       // its requests in flight at once.
-      constexpr int kC = D / 8, kStep = 256 / kC, kN = 2 * kQRows / kStep;
+      // Few rows: every warp's 32 TMEM lanes get the same ones.
+      constexpr int kC = D / 8, kStep = 256 / kC, kN = (FEW ? 1 : 2) * kQRows / kStep;
+      constexpr int kLoads = FEW ? kFewRows / kStep : kN;
       const int c = stid % kC, r0 = stid / kC;
-      uint4 v[kN];
+      uint4 v[kLoads];
 #pragma unroll
-      for (int k = 0; k < kN; ++k) {
+      for (int k = 0; k < kLoads; ++k) {
         const int gr = g.qt0 * kQRows + r0 + k * kStep;
         v[k] = make_uint4(0, 0, 0, 0);
-        if (gr < p.rows && (dual || k < kN / 2))
+        if (gr < p.rows && (FEW || dual || k < kN / 2))
           v[k] = __ldg(reinterpret_cast<const uint4*>(p.q + query_row(p, b, hk, gr) * D) + c);
       }
       constexpr int kW = kMaxRows / 32;
@@ -662,9 +684,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
         const int row = r0 + k * kStep, rr = row & (kQRows - 1);
-        if (dual || k < kN / 2)
+        if (FEW || dual || k < kN / 2)
           *reinterpret_cast<uint4*>(q_s + (row / kQRows) * kQTile + (c >> 3) * kQHalf + rr * 128 +
-                                    (((c & 7) ^ (rr & 7)) << 4)) = v[k];
+                                    (((c & 7) ^ (rr & 7)) << 4)) = v[k % kLoads];
       }
 #pragma unroll
       for (int i = 0; i < kW; ++i) sh->anc[stid][i] = a[i];
@@ -690,6 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const int key0 = g.first + (nt - 1 - j) * kKeys;  // of the sequence
+      const int wkey0 = key0 + (FEW ? (warp & 3) * 16 : 0);  // of the warp's chunks
       // S is read: the next S may be formed while this one's weights are
       auto free_s = [&]() {
         tc_fence_before();
@@ -704,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       bool s_kept = true;
       if (warp_live) {
-        const bool edge = __any_sync(0xffffffffu, key0 + kKeys > g.kl || key0 < lo);
+        const bool edge = __any_sync(0xffffffffu, wkey0 + kChunks * 16 > g.kl || wkey0 < lo);
         bool done = false;
         // A tile inside the prefix: the exponents with the reference at hand, in one
         // pass.  The general path takes over if a row has no reference yet (no key so
@@ -714,11 +737,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float sub = m;
           const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
           const uint64_t step2 = f2_pack(2.f * slope2, 2.f * slope2);
-          uint32_t x[kKeys / 16][16];
+          uint32_t x[kChunks][16];
 #pragma unroll
-          for (int c = 0; c < kKeys / 16; ++c) tmem_ld16(t_s + c * 16, x[c]);
+          for (int c = 0; c < kChunks; ++c) tmem_ld16(t_s + c * 16, x[c]);
 #pragma unroll
-          for (int c = 0; c < kKeys / 16; ++c) tmem_wait_ld16(x[c]);
+          for (int c = 0; c < kChunks; ++c) tmem_wait_ld16(x[c]);
           // exponents of a pair of keys
           auto exponents = [&](int c, int e, float base, uint64_t& add, float& a0, float& a1) {
             const uint64_t v = f2_pack(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1]));
@@ -739,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float am[2] = {0.f, 0.f}, sm[2] = {-INFINITY, -INFINITY};
           if (CAP || !BIAS) {
 #pragma unroll
-            for (int c = 0; c < kKeys / 16; ++c)
+            for (int c = 0; c < kChunks; ++c)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const float x0 = __uint_as_float(x[c][2 * e]), x1 = __uint_as_float(x[c][2 * e + 1]);
@@ -749,8 +772,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (BIAS) {
 #pragma unroll
-            for (int c = 0; c < kKeys / 16; ++c) {
-              const float base = -slope2 * (float)(pos - key0 - 16 * c) - sub;
+            for (int c = 0; c < kChunks; ++c) {
+              const float base = -slope2 * (float)(pos - wkey0 - 16 * c) - sub;
               uint64_t add = 0;
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
@@ -770,10 +793,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             free_s();
             s_kept = false;
             done = true;
-            uint32_t pk[kKeys / 16][8];
+            uint32_t pk[kChunks][8];
             uint64_t sub2 = f2_pack(-sub, -sub);
 #pragma unroll
-            for (int c = 0; c < kKeys / 16; ++c)
+            for (int c = 0; c < kChunks; ++c)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 float a0 = __uint_as_float(x[c][2 * e]), a1 = __uint_as_float(x[c][2 * e + 1]);
@@ -787,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
 #pragma unroll
-            for (int c = 0; c < kKeys / 16; ++c) tmem_st8(t_p + c * 8, pk[c]);
+            for (int c = 0; c < kChunks; ++c) tmem_st8(t_p + c * 8, pk[c]);
           }
         }
         if (!done) {
@@ -821,16 +844,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto scores = [&](int c, float sub, float (&x)[16]) {
             uint32_t raw[16];
             tmem_ld16(t_s + c * 16, raw);
-            const uint32_t ok = edge ? allowed(key0 + 16 * c) : ~0u;
+            const uint32_t ok = edge ? allowed(wkey0 + 16 * c) : ~0u;
             tmem_wait_ld16(raw);
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(raw[e]);
-            chunk_scores<MODE>(x, p, edge, ok, sub, slope2, pos, key0 + 16 * c, g.kl, p.M, sh->depth);
+            chunk_scores<MODE>(x, p, edge, ok, sub, slope2, pos, wkey0 + 16 * c, g.kl, p.M, sh->depth);
           };
           if (TRACK) {  // first the maximum; the scores wait in S's place
             float mx = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < kKeys / 16; ++c) {
+            for (int c = 0; c < kChunks; ++c) {
               float x[16];
               scores(c, 0.f, x);
               float a[2] = {fmaxf(mx, x[0]), x[1]};
@@ -876,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float sub = m == -INFINITY ? 0.f : m;
 #pragma unroll 1
-          for (int c = 0; c < kKeys / 16; ++c) {
+          for (int c = 0; c < kChunks; ++c) {
             float x[16];
             if (TRACK) {
               uint32_t raw[16];
@@ -977,7 +1000,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = mm;
       }
     }
-    if (dual || pipe == 0) {
+    if (FEW && pipe == 0) {
+      // The warps' parts of the keys join as well: each row's four sums of O, then the
+      // D / 8 columns of all rows dealt to the pipe's threads.
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (have) {
+          tmem_ld32(t_o + c * 32, o);
+          tmem_wait_ld32(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float4& x = join_o[(c * 8 + e) * kQRows + r];
+          x = make_float4(fmaf(x.x, w1, __uint_as_float(o[4 * e]) * w0), fmaf(x.y, w1, __uint_as_float(o[4 * e + 1]) * w0),
+                          fmaf(x.z, w1, __uint_as_float(o[4 * e + 2]) * w0),
+                          fmaf(x.w, w1, __uint_as_float(o[4 * e + 3]) * w0));
+        }
+      }
+      sh->join_ml[r] = make_float2(m, l);
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      for (int e = r; e < p.rows * (D / 8); e += kQRows) {
+        const int c = e / p.rows, row = e - c * p.rows;
+        float2 ml[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ml[i] = sh->join_ml[32 * i + row];
+        const float mm = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), ms = mm == -INFINITY ? 0.f : mm;
+        float sum = 0.f;
+        float4 a[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w = fast_exp2(ml[i].x - ms);
+          sum = fmaf(ml[i].y, w, sum);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 x = join_o[(2 * c + h) * kQRows + 32 * i + row];
+            a[h] = make_float4(fmaf(x.x, w, a[h].x), fmaf(x.y, w, a[h].y), fmaf(x.z, w, a[h].z), fmaf(x.w, w, a[h].w));
+          }
+        }
+        if (g.whole) {
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          reinterpret_cast<uint4*>(p.out + query_row(p, b, hk, row) * D)[c] =
+              make_uint4(pack_bf16x2(a[0].x * inv, a[0].y * inv), pack_bf16x2(a[0].z * inv, a[0].w * inv),
+                         pack_bf16x2(a[1].x * inv, a[1].y * inv), pack_bf16x2(a[1].z * inv, a[1].w * inv));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.ws_o) + (int64_t)g.rec * (D / 4) * p.rec_rows;
+          __stcg(dst + (2 * c) * p.rec_rows + row, a[0]);
+          __stcg(dst + (2 * c + 1) * p.rec_rows + row, a[1]);
+          if (c == 0) __stcg(p.ws_ml + (int64_t)g.rec * p.rec_rows + row, make_float2(mm, sum));
+        }
+      }
+    }
+    if (!FEW && (dual || pipe == 0)) {
       const bool whole = g.whole;
       const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
       w0 *= inv;
@@ -1111,23 +1188,23 @@ __global__ void __launch_bounds__(256) scored_merge_kernel(const __grid_constant
   }
 }
 
-// [BH][S_cap][D] bf16 in boxes of kKeys rows: 64 columns (D = 64), or both 64-column
+// [BH][S_cap][D] bf16 in boxes of `keys` rows: 64 columns (D = 64), or both 64-column
 // halves of a row (D = 128), landing as [half][row][128 B], 128-byte swizzle.
-bool encode_scored_map(CUtensorMap* map, const void* base, int64_t BH, int64_t S_cap, int D) {
+bool encode_scored_map(CUtensorMap* map, const void* base, int64_t BH, int64_t S_cap, int D, int keys) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return false;
   const cuuint64_t S = (cuuint64_t)std::max<int64_t>(S_cap, 1);
   if (D == 128) {
     cuuint64_t dims[4] = {64, S, 2, (cuuint64_t)BH};
     cuuint64_t strides[3] = {256, 128, S * 256};
-    cuuint32_t box[4] = {64, (cuuint32_t)kKeys, 2, 1}, estr[4] = {1, 1, 1, 1};
+    cuuint32_t box[4] = {64, (cuuint32_t)keys, 2, 1}, estr[4] = {1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   }
   cuuint64_t dims[3] = {64, S, (cuuint64_t)BH};
   cuuint64_t strides[2] = {128, S * 128};
-  cuuint32_t box[3] = {64, (cuuint32_t)kKeys, 1}, estr[3] = {1, 1, 1};
+  cuuint32_t box[3] = {64, (cuuint32_t)keys, 1}, estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1135,7 +1212,7 @@ bool encode_scored_map(CUtensorMap* map, const void* base, int64_t BH, int64_t S
 
 // Grid and workspace of a shape (lengths are known on the device only).
 struct ScoredPlan {
-  int grid, nqt, npairs, merge, rec_rows;
+  int few, grid, nqt, npairs, merge, rec_rows;
   size_t ml_off, row_off, ws_bytes;  // records, (reference, sum) pairs, rows' CTAs
 };
 
@@ -1147,11 +1224,13 @@ tv_status plan_scored(int B, int M, int Hq, int Hkv, int D, int64_t S_cap, int w
   int64_t keys = std::max<int64_t>(S_cap, 1);
   if (window > 0) keys = std::min<int64_t>(keys, (int64_t)window - 1 + M + 1);
   // shorter rows are never cut
-  const int64_t tiles = (keys + kKeys - 1) / kKeys;
   // the dealing counts the key tiles of all rows of work in 31 bits
-  if ((double)tiles * Hkv * B * lp.nqt > (double)(1 << 30)) return TV_ERR_UNSUPPORTED;
+  if ((double)((keys + keys_of(true) - 1) / keys_of(true)) * Hkv * B * lp.nqt > (double)(1 << 30))
+    return TV_ERR_UNSUPPORTED;
   const tv_status r = current_sms(lp.grid);
   if (r != TV_OK) return r;
+  lp.few = rows <= kFewRows && keys * B * Hkv <= (int64_t)kFewKeys * lp.grid;
+  const int64_t tiles = (keys + keys_of(lp.few) - 1) / keys_of(lp.few);
   lp.merge = tiles >= 2 * kMinTiles;
   const size_t recs = lp.merge ? 4 * (size_t)lp.grid * lp.rec_rows : 0;
   lp.ml_off = recs * D * sizeof(float);
@@ -1160,14 +1239,19 @@ tv_status plan_scored(int B, int M, int Hq, int Hkv, int D, int64_t S_cap, int w
   return TV_OK;
 }
 
+template <int D, bool FEW>
+auto scored_kernel_of(int mode) {
+  return mode == kPlain     ? scored_kernel<D, kPlain, FEW>
+         : mode == kCapLow  ? scored_kernel<D, kCapLow, FEW>
+         : mode == kCapHigh ? scored_kernel<D, kCapHigh, FEW>
+         : mode == kBias    ? scored_kernel<D, kBias, FEW>
+                            : scored_kernel<D, kCapBias, FEW>;
+}
+
 template <int D>
 tv_status launch_scored(int mode, const CUtensorMap& tmk, const CUtensorMap& tmv, const ScoredParams& p,
                         const ScoredPlan& lp, cudaStream_t s) {
-  auto kern = mode == kPlain     ? scored_kernel<D, kPlain>
-              : mode == kCapLow  ? scored_kernel<D, kCapLow>
-              : mode == kCapHigh ? scored_kernel<D, kCapHigh>
-              : mode == kBias    ? scored_kernel<D, kBias>
-                                 : scored_kernel<D, kCapBias>;
+  auto kern = lp.few ? scored_kernel_of<D, true>(mode) : scored_kernel_of<D, false>(mode);
   const size_t smem = 2 * (D / 64) * kQHalf + kRingBytes + sizeof(Shared);
   tv_status r = allow_shared(reinterpret_cast<const void*>(kern), (int)smem);
   if (r != TV_OK) return r;
@@ -1266,7 +1350,8 @@ extern "C" tv_status tree_attention_scored(const uint16_t* q, const uint16_t* k,
   CUtensorMap tmk, tmv;
   const int64_t BH = (int64_t)p.n_slots * Hkv;
   if (BH > 0x7fffffffLL) return TV_ERR_UNSUPPORTED;
-  if (!encode_scored_map(&tmk, k, BH, S_cap, D) || !encode_scored_map(&tmv, v, BH, S_cap, D))
+  if (!encode_scored_map(&tmk, k, BH, S_cap, D, keys_of(lp.few)) ||
+      !encode_scored_map(&tmv, v, BH, S_cap, D, keys_of(lp.few)))
     return record_cuda_error(cudaErrorInvalidValue);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return D == 64 ? launch_scored<64>(mode, tmk, tmv, p, lp, s) : launch_scored<128>(mode, tmk, tmv, p, lp, s);
