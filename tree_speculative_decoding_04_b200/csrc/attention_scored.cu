@@ -37,8 +37,11 @@
 // With few query rows a tile has 64 keys and its softmax is shared by a pipe's four
 // warps (kFewRows).
 // What bounds it: the softmax warps, two to a scheduler, 1.3-1.45 us per pair of tiles
-// (MUFU 45-57 %, tensor pipe 45-54 %).  Four to a scheduler, each with half of a row's
-// columns, took 616 us: twice the TMEM accesses at half the width.
+// (tensor pipe 42 %, MUFU 39 %).  Four to a scheduler, each with half of a row's
+// columns, took 616 us: twice the TMEM accesses at half the width.  (510 us now, 680
+// TFLOP/s, 0.40 of a plain bf16 GEMM's rate; a window of 4096 keys for 6 x 4 rows x 8 heads x 8
+// sequences, 135 MB, 36.7 us: 3.7 TB/s with 5 us before the first tile and 6 us of
+// epilogue and merge.)
 #include <algorithm>
 #include <climits>
 

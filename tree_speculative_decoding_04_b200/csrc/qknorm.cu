@@ -10,8 +10,10 @@
 //   y = x / sqrt(mean(x^2) + eps) * (offset + w)
 //   (y[i], y[i + R/2]) turns by (kv_len + depth[u]) * theta^(-2i/R), i < R/2
 //
-// Bound by HBM for large batches (each element is read once and written once),
-// by the launch for small ones.
+// Each element is read once and written once: 84.6 MB for 16 x 129 rows of 64 + 8 + 8
+// heads of 128, which take 20 us (4.2 TB/s, 13.1 us at the copy rate; instruction issue
+// 70 % busy: the conversions, weights and rotation of 16 elements a lane).  A single token
+// takes 3.3 us, a launch's length.
 #include <algorithm>
 
 #include "tv_common.cuh"
