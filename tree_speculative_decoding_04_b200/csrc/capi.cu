@@ -30,7 +30,7 @@ std::map<int, int> g_sms;                                   // by device
 std::map<std::pair<int, const void*>, int> g_shared_bytes;  // by device and kernel
 }  // namespace
 
-tv_status current_sms(int& sms) {
+tv_status current_sms(int& sms) try {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return record_cuda_error(e);
@@ -44,9 +44,11 @@ tv_status current_sms(int& sms) {
   if (e != cudaSuccess) return record_cuda_error(e);
   g_sms[dev] = sms;
   return TV_OK;
+} catch (...) {  // (no memory for the table: nothing may leave a C entry point)
+  return record_cuda_error(cudaErrorMemoryAllocation);
 }
 
-tv_status allow_shared(const void* kernel, int bytes) {
+tv_status allow_shared(const void* kernel, int bytes) try {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return record_cuda_error(e);
@@ -57,6 +59,8 @@ tv_status allow_shared(const void* kernel, int bytes) {
   if (e != cudaSuccess) return record_cuda_error(e);
   have = bytes;
   return TV_OK;
+} catch (...) {
+  return record_cuda_error(cudaErrorMemoryAllocation);
 }
 
 }  // namespace tv
