@@ -1,0 +1,91 @@
+"""GPU tests of the operators where their arithmetic comes to its limits:
+temperatures near zero and masked vocabularies."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import dev
+from operator_helpers import parents
+from test_gpu_operators import _check_sample, _sample
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------------------- temperatures and fills
+
+TEMPERATURES = [1e-6, 1e-7, 1e-8, 5e-9, 1e-9, 1e-12, 1e-18, 1e-20, 1e-25, 1e-30, 1e-45, 1e-3]
+FILTERS = [(None, None, None), (None, 0.9, None), (None, 0.5, 0.2), (None, None, 0.3), (40, 0.95, None)]
+
+
+def _filters(B, k, p, m):
+    return ([k] * B if k else None), ([p] * B if p else None), ([m] * B if m else None)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("k,p,m", FILTERS)
+def test_accept_sample_near_zero_temperature(orc, k, p, m, bf16):
+    """Row maxima from 1 to 100 and around zero, alone, with neighbours one float below, and shared by tokens of
+    several chunks."""
+    rng = np.random.default_rng(21)
+    B, M, V = len(TEMPERATURES), 8, 5000
+    par = parents(B, M, 9, rng)
+    x = rng.normal(0, 2, (B, M + 1, V)).astype(np.float32)
+    for r in range(M + 1):
+        top = [1.0, 7.3, 24.7, 59.9, 100.0, 0.0, 3e-5, 12.5, 33.3][r]
+        if r in (5, 6):
+            x[:, r] = -np.abs(x[:, r])
+        x[:, r] = np.minimum(x[:, r], np.float32(top) - np.float32(0.5))
+        at = rng.permutation(V)[:8]
+        x[:, r, at[0]] = top
+        if r in (3, 4, 6, 7, 8):
+            x[:, r, at[1:5]] = top
+        if r in (2, 4, 8):
+            x[:, r, at[5:8]] = np.nextafter(np.float32(top), np.float32(0))
+    lx = torch.as_tensor(x, device=dev())
+    lx = lx.to(torch.bfloat16) if bf16 else lx
+    u = rng.random((B, M + 1)).astype(np.float32)
+    u[:, 7], u[:, 8] = 0.0, 1.0 - 2.0 ** -24
+    draft = lx.float().argmax(-1).cpu().numpy().astype(np.int32)
+    draft = np.stack([draft[b, par[b]] for b in range(B)])
+    got = _sample(lx, u, TEMPERATURES, par, draft, 9, *_filters(B, k, p, m))
+    assert ((got[0] >= 0) & (got[0] < V)).all()
+    _check_sample(orc, lx, u, TEMPERATURES, par, draft, 9, *_filters(B, k, p, m), got=got)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T", [1e-3, 1e-8, 1e-20])
+def test_accept_sample_near_zero_temperature_of_flat_rows(orc, T, bf16):
+    """Thousands of equal maxima: more than a short list holds, and the borders of top-p and top-k among them."""
+    rng = np.random.default_rng(22)
+    B, M, V = 2, 1, 60000
+    par = parents(B, M, 9, rng)
+    x = torch.as_tensor(rng.integers(37, 39, (B, M + 1, V)).astype(np.float32), device=dev())
+    x = x.to(torch.bfloat16) if bf16 else x
+    u = rng.random((B, M + 1)).astype(np.float32)
+    draft = np.zeros((B, M + 1), np.int32)
+    for k, p, m in ((None, None, None), (None, 0.7, None), (20000, None, None), (20000, 0.3, 0.5)):
+        _check_sample(orc, x, u, [T, T], par, draft, 9, *_filters(B, k, p, m))
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("fill", [-1e4, -1e18, -1e20, -1e25, -1e30, -3.3895314e38])
+def test_accept_sample_masked_vocabulary(orc, fill, bf16):
+    """Most of the vocabulary holds one large negative number: whole chunks of it, a chunk with one token left, a
+    padded end, and a row that holds nothing else."""
+    rng = np.random.default_rng(23)
+    B, M, V = 10, 3, 6500
+    par = parents(B, M, 9, rng)
+    x = rng.normal(0, 3, (B, M + 1, V)).astype(np.float32)
+    x[:, :, 1024:3072] = fill
+    x[:, 1, 3072:4096] = fill
+    x[:, 1, 3500] = 4.0
+    x[:, :, 5100:] = fill
+    x[:, 3] = fill
+    x[:5, 2, :1024] = fill  # the first live chunk is not the row's first
+    lx = torch.as_tensor(x, device=dev())
+    lx = lx.to(torch.bfloat16) if bf16 else lx
+    u = rng.random((B, M + 1)).astype(np.float32)
+    T = np.linspace(0.3, 1.5, B)
+    draft = rng.integers(0, 1024, (B, M + 1)).astype(np.int32)
+    for k, p, m in FILTERS:
+        _check_sample(orc, lx, u, T, par, draft, 9, *_filters(B, k, p, m))

@@ -33,11 +33,12 @@
 //           of the tokens in the border's bins and exact sums of what each chunk keeps
 //           for sure; the last block of a row settles the list and draws
 //   walk    tree_accept's acceptance walk, on the drawn tokens
-// Weights are doubles (2^((l - m) log2e / T), relative error below 2^-48: a
-// token's share of a flat vocabulary is 2^-18, and a sum in fp32 would move the
-// borders between tokens by as much).  The finish's histograms hold them as 64-bit
-// fixed-point numbers, and all other sums run in a fixed order, so results do not depend on
-// the order of the work.
+// Weights are doubles: a token's share of a flat vocabulary is 2^-18, and a sum in fp32
+// would move the borders between tokens by as much.  A weight 2^-e has a relative error
+// below 2^-48 (1 + e / 16): the series' remainder is 2^-48.6, and the roundings of l - m and
+// of log2e / T move the exponent by 2^-51.5 e at most.  The finish's histograms hold weights
+// as 64-bit fixed-point numbers in units of 2^-46 (2^-45 beyond 2^17 tokens), and all other
+// sums run in a fixed order, so results do not depend on the order of the work.
 //
 // What bounds it.  16 x 129 rows of 128256 fp32 logits (1059 MB, 164 us at the copy rate)
 // take 250 us with min-p and 300 us with top-k (one pass, 4 TB/s and the finish), 409 us
@@ -133,45 +134,50 @@ __device__ __forceinline__ void fill_table(double* tab) {
   for (int i = threadIdx.x; i < kTab * kTabCopies; i += kThreads) tab[i] = exp2((double)(i / kTabCopies) / kTab);
 }
 
-// 2^y for -1000 <= y <= 0: y = n / 32 + r, |r| <= 1/64; 2^r by the first
-// six terms of its series (the next is below 2^-48 of the result), 2^(n / 32) from
-// the table and the exponent field.
-__device__ __forceinline__ double pow2_in_range(double y, const double* tab) {
+// 2^(d c) for -1000 <= d c <= 0, c32 = 32 c: 32 d c = n + r, |r| <= 1/2, with r formed
+// from d in one rounding; 2^(r / 32) by the first six terms of its series (the next is
+// below 2^-48 of the result), 2^(n / 32) from the table and the exponent field.
+__device__ __forceinline__ double pow2_in_range(double d, double c32, const double* tab) {
   const double magic = 6755399441055744.0;  // 1.5 * 2^52: rounds to an integer
-  const double t = fma(y, (double)kTab, magic);
+  const double t = fma(d, c32, magic);
   const int n = __double2loint(t);
-  const double r = fma(t - magic, -1.0 / kTab, y);
-  double q = 0.0013333558146428443;  // ln2^5 / 120
-  q = fma(q, r, 0.0096181291076284772);
-  q = fma(q, r, 0.055504108664821580);
-  q = fma(q, r, 0.24022650695910071);
-  q = fma(q, r, 0.69314718055994531);
+  const double r = fma(d, c32, magic - t);
+  // ln2^i / i! / 32^i
+  double q = 0.0013333558146428443 / 33554432.0;
+  q = fma(q, r, 0.0096181291076284772 / 1048576.0);
+  q = fma(q, r, 0.055504108664821580 / 32768.0);
+  q = fma(q, r, 0.24022650695910071 / 1024.0);
+  q = fma(q, r, 0.69314718055994531 / 32.0);
   const double v = tab[(n & (kTab - 1)) * kTabCopies + (threadIdx.x & (kTabCopies - 1))] * fma(q, r, 1.0);
   return __hiloint2double(__double2hiint(v) + (n >> 5) * (1 << 20), __double2loint(v));
 }
 
 // Weight of logit x relative to the maximum m, c = log2(e) / T; 0 below 2^-1000.
+// The distance to the maximum comes first: c has no bound (T may be as small as a
+// float goes), so a product of c with x or m alone would lose the difference.
 __device__ __forceinline__ double weight(float x, float m, double c, const double* tab) {
   if (x == m) return x == -INFINITY ? 0.0 : 1.0;
   if (x == -INFINITY || m == INFINITY) return 0.0;
-  const double y = ((double)x - (double)m) * c;
-  return y > -1000.0 ? pow2_in_range(y, tab) : 0.0;
+  const double d = (double)x - (double)m;
+  return d * c > -1000.0 ? pow2_in_range(d, kTab * c, tab) : 0.0;
 }
 
-// The same without branches, for many tokens of one finite maximum: the exponent
-// is formed in one rounding, and what lies 900 octaves below the maximum (-inf and
-// NaN among it) counts as if it lay there.
+// The same without branches, for many tokens of one finite maximum: what lies 900
+// octaves below the maximum (-inf and NaN among it) counts as if it lay there.
 struct Weigher {
-  double c, off;
+  double m, c32;
   float far;
-  // (not where 900 octaves below the maximum is beyond the finite floats)
-  static __device__ __forceinline__ bool fits(float m, double c) { return m < INFINITY && (double)m - 900.0 / c > -1e38; }
-  __device__ __forceinline__ Weigher(float m, double c_) : c(c_) {
-    off = -(double)m * c_;
-    far = (float)((double)m - 900.0 / c_);
+  // Not where 900 octaves below the maximum is beyond the finite floats, and not where
+  // they span fewer than 128 steps of the floats at m: `far`, rounded to a float, would be
+  // the maximum itself, or more than 1000 octaves below it.
+  static __device__ __forceinline__ bool fits(float m, double c) {
+    return m < INFINITY && (double)m - 900.0 / c > -1e38 && fabs((double)m) * c < 900.0 * 65536.0;
+  }
+  __device__ __forceinline__ Weigher(float m_, double c) : m((double)m_), c32(kTab * c) {
+    far = (float)((double)m_ - 900.0 / c);
   }
   __device__ __forceinline__ double operator()(float x, const double* tab) const {
-    return pow2_in_range(fma((double)fmaxf(x, far), c, off), tab);
+    return pow2_in_range((double)fmaxf(x, far) - m, c32, tab);
   }
 };
 
@@ -438,7 +444,7 @@ __device__ void draw(const SampleParams& p, Shared& sh, int64_t row, double own,
   const double target = (double)p.uniform[row] * total;
   if (tid == 0) {
     sh.found = sh.found2 = INT_MAX;
-    sh.last = sh.last2 = -1;
+    sh.last = sh.last2 = 0;  // (a row's maximum weighs 1; whatever the sums are, an index stays inside the row)
   }
   __syncthreads();
   if (own > 0.0) {
