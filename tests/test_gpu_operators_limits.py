@@ -1,12 +1,13 @@
 """GPU tests of the operators where their arithmetic comes to its limits:
-temperatures near zero and masked vocabularies."""
+temperatures near zero, masked vocabularies, and waits that give up."""
 import numpy as np
 import pytest
 import torch
 
-from gpu_helpers import dev
+import tree_speculative_decoding_04_b200 as tv
+from gpu_helpers import dev, gpu_mask, i32
 from operator_helpers import parents
-from test_gpu_operators import _check_sample, _sample
+from test_gpu_operators import _attend, _attn_case, _check_attn, _check_sample, _sample
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +90,37 @@ def test_accept_sample_masked_vocabulary(orc, fill, bf16):
     draft = rng.integers(0, 1024, (B, M + 1)).astype(np.int32)
     for k, p, m in FILTERS:
         _check_sample(orc, lx, u, T, par, draft, 9, *_filters(B, k, p, m))
+
+
+# ----------------------------------------------------------------------------- waits that give up
+
+@pytest.mark.parametrize("B,M,Hq,Hkv,D,lens", [
+    (60, 1, 8, 2, 128, [i * 53 % 1300 for i in range(60)]),  # few rows
+    (12, 15, 8, 1, 64, [i * 531 % 6000 for i in range(12)]),  # a lone query tile
+    (20, 40, 16, 2, 128, [i * 53 % 1900 for i in range(20)]),  # a pair and a lone tile of each kv head
+])
+def test_attention_scored_short_limits_leave_no_copies_behind(B, M, Hq, Hkv, D, lens):
+    """Launches whose waits give up between launches that work in the shared memory they leave: the latter are right."""
+    q, k, v, ks, kl, par = _attn_case(B, M, Hq, Hkv, D, lens, 40)
+    ref, _ = _attend(q, k, v, ks, kl, par, softcap=50.0)
+    _check_attn(ref, q, k, v, ks, kl, par, softcap=50.0)
+    _, anc, depth, status = gpu_mask(par, 1000)
+    ks, kl = i32(ks), i32(kl)
+    ws = tv.attention_scored_workspace(B, M, Hq, Hkv, D, k.shape[2], 0, q.device)
+    flagged, outs = [], []
+    try:
+        for limit in (1, 500, 1000, 2000, 3000, 4000):
+            for _ in range(25):
+                for ns in (limit, 0):
+                    tv.set_wait_limit_ns(ns)
+                    out, st = torch.full_like(q, 7.0), torch.zeros_like(status)
+                    tv.tree_attention_scored(q, k, v, ks, kl, anc, depth, st, out, ws, softcap=50.0)
+                    if ns:
+                        flagged.append(st)
+                    else:
+                        outs.append((out, st))
+            assert all(torch.equal(out, ref) and int(st.abs().sum()) == 0 for out, st in outs)
+            outs.clear()
+    finally:
+        tv.set_wait_limit_ns(0)
+    assert any(int(st.sum()) > 0 for st in flagged)

@@ -199,7 +199,6 @@ struct Shared {
   uint64_t item_full[2], item_empty[2];
   uint64_t drain;
   uint32_t tmem;
-  int failed;
   Item item[2];
   float2 join_ml[kQRows];
   float depth[kMaxRows];
@@ -296,7 +295,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    sh->failed = 0;
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], 2);
@@ -559,12 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (failed && lane == 0) atomicExch(&sh->failed, 1);
       }
-      // a copy that no MMA waited for must land before the shared memory is released
-      if (failed || __any_sync(0xffffffffu, *(volatile int*)&sh->failed))
-        for (uint32_t i = 1; i <= (uint32_t)kSlots && i <= idx; ++i)
-          mbar_wait(&sh->full[(idx - i) % kSlots], ((idx - i) / kSlots) & 1);
+      // Every copy must land before the shared memory is released, one that no MMA waits
+      // for as well: a pipe may still give up after this warp is through.
+      for (uint32_t i = 1; i <= (uint32_t)kSlots && i <= idx; ++i)
+        mbar_wait(&sh->full[(idx - i) % kSlots], ((idx - i) / kSlots) & 1);
     } else if (lane == 0) {
       // -------------------------------------------------------------- MMA issue, one thread per pipe
       const int q = warp - 2;
@@ -628,7 +625,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit(&sh->empty[s]);
         }
         ok = ok && see(2 * it.nt - 1);
-        if (!ok) atomicExch(&sh->failed, 1);
         ++busy;
         base += 2 * it.nt;
         step0 += steps;
@@ -958,10 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (n > 0 && !to && !mbar_wait(&sh->pv_done[pipe], (step0 + n - 1) & 1, lim)) to = true;
     to = __any_sync(0xffffffffu, to);
     const bool have = n > 0 && !to;
-    if (to && lane == 0) {
-      atomicExch(&sh->failed, 1);
-      atomicOr(&p.status[b], kSeqTimeout);
-    }
+    if (to && lane == 0) atomicOr(&p.status[b], kSeqTimeout);
     tc_fence_after();
     if (!have) {
       m = -INFINITY;
