@@ -223,7 +223,8 @@ tv_status tree_attention_noalloc(const uint16_t* q, const uint16_t* k, const uin
  *             as for tree_attention: no initialisation, dead after the call, not
  *             shared by calls (or captured graphs) that overlap on the device
  *   everything else as for tree_attention, head dims 64 and 128 alike; a row
- *   without a key gets zeros.
+ *   without a key gets zeros.  After a wait that ran out (TV_SEQ_TIMEOUT) every
+ *   row of the sequence is either zero or complete.
  * Contract: the K/V rows that some query row of the sequence may read hold
  * finite values; prefix columns before the root's window are not used, whatever
  * they hold.

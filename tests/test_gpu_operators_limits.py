@@ -124,3 +124,40 @@ def test_attention_scored_short_limits_leave_no_copies_behind(B, M, Hq, Hkv, D, 
     finally:
         tv.set_wait_limit_ns(0)
     assert any(int(st.sum()) > 0 for st in flagged)
+
+
+@pytest.mark.parametrize("B,M,Hq,Hkv,D,lens", [
+    (3, 3, 8, 1, 64, [700, 60, 250]),            # few rows, short keys: rows never cut
+    (5, 1, 16, 4, 128, [900, 30, 700, 150, 880]),  # few rows, whole ones
+    (2, 3, 8, 1, 128, [9000, 5000]),             # few rows, cut between CTAs
+    (60, 9, 16, 2, 64, [i * 37 % 700 for i in range(60)]),  # a lone tile of 80 rows, several items to a CTA
+    (2, 15, 8, 1, 128, [6000, 3100]),            # a lone tile, cut between CTAs
+    (40, 40, 16, 2, 128, [i * 53 % 900 for i in range(40)]),  # a pair and a lone tile of each kv head
+])
+def test_attention_scored_rows_are_zero_or_complete_after_a_wait_ran_out(B, M, Hq, Hkv, D, lens):
+    """Limits from nothing to a step's length, many launches: whichever warp gives up first, a flagged sequence has no
+    row that lacks some of its keys, and the others are right."""
+    q, k, v, ks, kl, par = _attn_case(B, M, Hq, Hkv, D, lens, 41)
+    ref, _ = _attend(q, k, v, ks, kl, par, softcap=50.0)
+    _check_attn(ref, q, k, v, ks, kl, par, softcap=50.0)
+    _, anc, depth, clean = gpu_mask(par, 1000)
+    ks, kl = i32(ks), i32(kl)
+    ws = tv.attention_scored_workspace(B, M, Hq, Hkv, D, k.shape[2], 0, q.device)
+    flagged = 0
+    try:
+        for limit in (1, 300, 1000, 2000, 4000):
+            tv.set_wait_limit_ns(limit)
+            for _ in range(40):
+                out, status = torch.full_like(q, 7.0), torch.zeros_like(clean)
+                tv.tree_attention_scored(q, k, v, ks, kl, anc, depth, status, out, ws, softcap=50.0)
+                same, zero = (out == ref).all(-1), (out == 0).all(-1)
+                assert bool((same | zero).all())
+                assert bool(((status == 0) | (status == tv.SEQ_TIMEOUT)).all())
+                assert bool(same.flatten(1).all(1)[status == 0].all())
+                flagged += int((status != 0).sum())
+    finally:
+        tv.set_wait_limit_ns(0)
+    assert flagged > 0
+    out, status = torch.full_like(q, 7.0), torch.zeros_like(clean)
+    tv.tree_attention_scored(q, k, v, ks, kl, anc, depth, status, out, ws, softcap=50.0)
+    assert torch.equal(out, ref) and int(status.abs().sum()) == 0

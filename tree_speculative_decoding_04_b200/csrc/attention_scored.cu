@@ -215,6 +215,20 @@ __device__ __forceinline__ int64_t query_row(const ScoredParams& p, int b, int h
   return ((int64_t)b * (p.M + 1) + node) * p.Hq + hk * p.G + (gr - node * p.G);
 }
 
+// Whether some thread of the 256 softmax threads says so (a barrier of them all).
+__device__ __forceinline__ bool any_of_softmax(bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, 3, 256, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)mine)
+      : "memory");
+  return any != 0;
+}
+
 // One capped score (log2) from the raw product x.
 __device__ __forceinline__ float cap_score(float x, const ScoredParams& p) {
   const float t = x * x;
@@ -502,9 +516,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item it = next();
         if (n >= 2 && !stuck)
           stuck = !__all_sync(0xffffffffu, mbar_wait(&sh->item_empty[n & 1], ((n >> 1) - 1) & 1, kListWait));
-        if (stuck) {  // nobody takes these any more; the merge still needs the rows' places
+        if (stuck) {  // nobody takes these any more: zero rows; the merge still needs the rows' places
           if (it.index < 0) break;
           if (lane == 0) atomicOr(&p.status[it.b], kSeqTimeout);
+          const int rows = it.whole ? min(it.dual ? 2 * kQRows : kQRows, p.rows - it.qt0 * kQRows) : 0;
+          for (int e = lane; e < rows * (D / 8); e += 32)
+            reinterpret_cast<uint4*>(p.out + query_row(p, it.b, it.hk, it.qt0 * kQRows + e / (D / 8)) * D)[e % (D / 8)] =
+                make_uint4(0, 0, 0, 0);
           continue;
         }
         if (lane == 0) {
@@ -953,9 +971,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (n > 0 && !to && !mbar_wait(&sh->pv_done[pipe], (step0 + n - 1) & 1, lim)) to = true;
     to = __any_sync(0xffffffffu, to);
-    const bool have = n > 0 && !to;
+    bool have = n > 0 && !to;
     if (to && lane == 0) atomicOr(&p.status[b], kSeqTimeout);
     tc_fence_after();
+    // Both pipes' products have read the query tile.  Where they shared it, a row is the sum
+    // of the two (with few rows, of all eight warps): if one gave up, none of it counts.
+    if (!dual && any_of_softmax(to)) have = false;
     if (!have) {
       m = -INFINITY;
       l = 0.f;
@@ -966,7 +987,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     float4* join_o = reinterpret_cast<float4*>(q_s);  // [D / 4][128]
     float w0 = 1.f, w1 = 0.f;
     if (!dual) {
-      asm volatile("bar.sync 3, 256;" ::: "memory");  // both pipes' products have read the query tile
       if (pipe == 1) {
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
