@@ -1,5 +1,6 @@
 """GPU tests of the operators where their arithmetic comes to its limits:
-temperatures near zero, masked vocabularies, and waits that give up."""
+temperatures near zero, masked vocabularies, waits that give up, calls in flight
+together, many rows."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +8,7 @@ import torch
 import tree_speculative_decoding_04_b200 as tv
 from gpu_helpers import dev, gpu_mask, i32
 from operator_helpers import parents
-from test_gpu_operators import _attend, _attn_case, _check_attn, _check_sample, _sample
+from test_gpu_operators import _attend, _attn_case, _check_attn, _check_sample, _norm_case, _sample
 
 pytestmark = pytest.mark.gpu
 
@@ -161,3 +162,63 @@ def test_attention_scored_rows_are_zero_or_complete_after_a_wait_ran_out(B, M, H
     out, status = torch.full_like(q, 7.0), torch.zeros_like(clean)
     tv.tree_attention_scored(q, k, v, ks, kl, anc, depth, status, out, ws, softcap=50.0)
     assert torch.equal(out, ref) and int(status.abs().sum()) == 0
+
+
+# ----------------------------------------------------------------------------- calls in flight together
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_accept_sample_calls_in_flight_together(orc, bf16):
+    """Calls queued on two streams with nothing between them, each stream with a workspace and outputs of its own;
+    rows of every kind, those with a flat top-p through all launches."""
+    rng = np.random.default_rng(51)
+    B, M, V = 12, 9, 30000
+    par = parents(B, M, 9, rng)
+    x = [torch.as_tensor(rng.normal(0, s, (B, M + 1, V)).astype(np.float32), device=dev()) for s in (0.4, 0.7)]
+    x = [t.to(torch.bfloat16) if bf16 else t for t in x]
+    u = [rng.random((B, M + 1)).astype(np.float32) for _ in x]
+    T = np.linspace(0.5, 1.4, B).astype(np.float32)
+    k = [0, 0, 0, 40, 0, 0, 9000, 0, 0, 0, 1, 0]
+    p = [0.95, 0.9, 1.0, 1.0, 0.99, 0.5, 0.9, 1.0, 0.999, 0.8, 0.3, 0.97]
+    m = [0, 0, 0, 0, 0.01, 0, 0, 0.2, 0, 0.05, 0, 0]
+    draft = rng.integers(0, V, (B, M + 1)).astype(np.int32)
+    ref = [_sample(x[i], u[i], T, par, draft, 9, k, p, m) for i in range(2)]
+    for i in range(2):
+        _check_sample(orc, x[i], u[i], T, par, draft, 9, k, p, m, got=ref[i])
+    parg, anc, depth, _ = gpu_mask(par, 9)
+    f32 = lambda a: torch.as_tensor(np.asarray(a, np.float32), device=dev())  # noqa: E731
+    settings = [f32(T), i32(k), f32(p), f32(m)]
+    streams, calls = [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(2):
+        ws = tv.accept_sample_workspace(B, M, V, dev())
+        e = lambda *s: torch.empty(s, dtype=torch.int32, device=dev())  # noqa: E731
+        outs = [(e(B, M + 1), torch.empty((B, M + 1), device=dev()), e(B), e(B, 10), e(B)) for _ in range(30)]
+        calls.append((ws, f32(u[i]), i32(draft), torch.zeros(B, dtype=torch.int32, device=dev()), outs))
+    torch.cuda.synchronize()
+    for r in range(30):
+        for i, s in enumerate(streams):
+            ws, ui, di, st, outs = calls[i]
+            tok, lp, al, path, bonus = outs[r]
+            tv.tree_accept_sample(x[i], ui, settings[0], di, parg, depth, anc, st, 9, tok, al, path, bonus, ws,
+                                  top_k=settings[1], top_p=settings[2], min_p=settings[3], logprob=lp, stream=s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for outs in calls[i][4]:
+            for got, want in zip(outs, ref[i][:5]):
+                np.testing.assert_array_equal(got.cpu().numpy(), want)
+
+
+def test_qk_norm_rope_of_many_rows():
+    """More rows than a GPU takes at once (fewer threads to a row), against the same rows a few at a time."""
+    B, M, Hq, Hkv, D = 37, 20, 6, 2, 128
+    qkv, wq, wk, k, v, ks, kl, par = _norm_case(B, M, Hq, Hkv, D, [7 * b for b in range(B)], 52, pad=8)
+    _, anc, depth, status = gpu_mask(par, 1000)
+    ks, kl = i32(ks), i32(kl)
+    for R in (D, 32):
+        got, want = [(torch.full((B, M + 1, Hq, D), 77.0, dtype=torch.bfloat16, device=dev()), k.clone(), v.clone())
+                     for _ in range(2)]
+        tv.tree_qk_norm_rope(qkv, wq, wk, *got, ks, kl, depth, eps=1e-5, rope_theta=5e5, rotary_dim=R)
+        for b in range(B):
+            tv.tree_qk_norm_rope(qkv[b:b + 1], wq, wk, want[0][b:b + 1], want[1][b:b + 1], want[2][b:b + 1],
+                                 ks[b:b + 1], kl[b:b + 1], depth[b:b + 1], eps=1e-5, rope_theta=5e5, rotary_dim=R)
+        for a, c in zip(got, want):
+            assert torch.equal(a, c)
