@@ -1,0 +1,17 @@
+"""TreeVerifier's settings, as far as they need no GPU."""
+import numpy as np
+import pytest
+
+import tree_speculative_decoding_04_b200 as tv
+from tree_speculative_decoding_04_b200.verifier import _layer_windows
+
+
+@pytest.mark.parametrize("window", [7, np.int64(7), np.int32(7), np.uint16(7), [7, 7, 7], np.array([7, 7, 7])])
+def test_a_window_is_any_integer_or_one_for_each_layer(window):
+    got = _layer_windows(window, 3)
+    assert got == [7, 7, 7] and all(type(w) is int for w in got)
+
+
+def test_a_window_for_each_layer_must_match_the_layers():
+    with pytest.raises(tv.TVError, match="window: 2 entries for 3 layers"):
+        _layer_windows([7, 0], 3)

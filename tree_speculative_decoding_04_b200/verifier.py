@@ -18,6 +18,7 @@ back in one copy.  Nothing here computes: it allocates, copies and calls.
 from __future__ import annotations
 
 import dataclasses
+import numbers
 
 import torch
 
@@ -28,6 +29,14 @@ _ALIGN = 256
 
 def _align(x: int) -> int:
     return (x + _ALIGN - 1) // _ALIGN * _ALIGN
+
+
+def _layer_windows(window, L):
+    """The window of every layer, from one for all (any integer type) or a sequence."""
+    windows = [int(window)] * L if isinstance(window, numbers.Integral) else [int(w) for w in window]
+    if len(windows) != L:
+        raise tv.TVError(f"window: {len(windows)} entries for {L} layers")
+    return windows
 
 
 class _InputLayout:
@@ -126,9 +135,7 @@ class TreeVerifier:
         self.k_commit_ptrs = tv.layer_pointers([self.k[i] for i in ids], dev)
         self.v_commit_ptrs = tv.layer_pointers([self.v[i] for i in ids], dev)
         self.softcap, self.alibi_slopes = float(softcap), alibi_slopes
-        self.window = [int(window)] * L if isinstance(window, int) else [int(w) for w in window]
-        if len(self.window) != L:
-            raise tv.TVError(f"window: {len(self.window)} entries for {L} layers")
+        self.window = _layer_windows(window, L)
         self.scored = [self.softcap > 0 or w > 0 or alibi_slopes is not None for w in self.window]
         if self.rope_theta > 0 and any(self.scored):
             raise tv.TVError("rope_theta: capped, windowed and biased attention take rotated queries (see norm_rope)")
