@@ -18,6 +18,7 @@ back in one copy.  Nothing here computes: it allocates, copies and calls.
 from __future__ import annotations
 
 import dataclasses
+import math
 import numbers
 
 import torch
@@ -36,6 +37,8 @@ def _layer_windows(window, L):
     windows = [int(window)] * L if isinstance(window, numbers.Integral) else [int(w) for w in window]
     if len(windows) != L:
         raise tv.TVError(f"window: {len(windows)} entries for {L} layers")
+    if min(windows, default=0) < 0:
+        raise tv.TVError(f"window: {min(windows)}, expected 0 (off) or a number of positions")
     return windows
 
 
@@ -104,6 +107,9 @@ class TreeVerifier:
         settings `temperature`, `top_k`, `top_p`, `min_p` [B] (1, off, off, off
         until the caller writes them); the draws are `argmax` (the token at every
         node) and `logprob`."""
+        self.softcap, self.alibi_slopes, self.window = float(softcap), alibi_slopes, _layer_windows(window, L)
+        if not 0 <= self.softcap < math.inf:  # (NaN as well: such a cap must not mean none)
+            raise tv.TVError(f"softcap: {softcap}, expected 0 (off) or a positive number")
         self.B, self.M, self.Hq, self.Hkv, self.D, self.V, self.L = B, M, Hq, Hkv, D, V, L
         self.S_cap, self.max_depth, self.realign = S_cap, max_depth, bool(realign)
         self.rope_theta = float(rope_theta)
@@ -134,8 +140,6 @@ class TreeVerifier:
         ids = list(range(L)) if commit_layers is None else list(commit_layers)
         self.k_commit_ptrs = tv.layer_pointers([self.k[i] for i in ids], dev)
         self.v_commit_ptrs = tv.layer_pointers([self.v[i] for i in ids], dev)
-        self.softcap, self.alibi_slopes = float(softcap), alibi_slopes
-        self.window = _layer_windows(window, L)
         self.scored = [self.softcap > 0 or w > 0 or alibi_slopes is not None for w in self.window]
         if self.rope_theta > 0 and any(self.scored):
             raise tv.TVError("rope_theta: capped, windowed and biased attention take rotated queries (see norm_rope)")
