@@ -1197,7 +1197,7 @@ tv_status launch_sample(const SampleParams& p, int sms, cudaStream_t s) {
 }  // namespace tv
 
 extern "C" size_t tree_accept_sample_workspace_size(int B, int M, int V) {
-  return B > 0 && M >= 0 && V > 0 ? tv::plan_sample(B, M, V).bytes : 0;
+  return B > 0 && M >= 0 && M < tv::kMaxRows && V > 0 && V <= tv::kMaxVocab ? tv::plan_sample(B, M, V).bytes : 0;
 }
 
 extern "C" tv_status tree_accept_sample(const void* logits, int logits_type, int64_t logits_stride,
