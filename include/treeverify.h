@@ -231,8 +231,9 @@ tv_status tree_attention_noalloc(const uint16_t* q, const uint16_t* k, const uin
  * TV_ERR_UNSUPPORTED: B > 4096, (Hq / Hkv) * (M + 1) >= 2^21, scale > 10^4 softcap,
  * more than 2^30 tiles: B * Hkv * ceil((Hq / Hkv) (M + 1) / 128) * ceil(K / 64) with
  * K = S_cap or, if less, window + M.
- * The softmax weights are rounded to bf16 before their product with V; scores,
- * sums and the merge of split key ranges are fp32.
+ * The softmax weights are rounded to bf16 before their product with V, and the
+ * row's sum takes them as rounded (a row is a mean of its V rows; with one key it
+ * is that key's V); scores, sums and the merge of split key ranges are fp32.
  */
 size_t tree_attention_scored_workspace_size(int B, int M, int Hq, int Hkv, int D, int64_t S_cap, int window);
 

@@ -1,6 +1,6 @@
 """GPU tests of the operators where their arithmetic comes to its limits:
 temperatures near zero, masked vocabularies, waits that give up, calls in flight
-together, many rows."""
+together, many rows, rows of few keys."""
 import numpy as np
 import pytest
 import torch
@@ -8,7 +8,7 @@ import torch
 import tree_speculative_decoding_04_b200 as tv
 from gpu_helpers import dev, gpu_mask, i32
 from operator_helpers import parents
-from test_gpu_operators import _attend, _attn_case, _check_attn, _check_sample, _norm_case, _sample
+from test_gpu_operators import _attend, _attn_case, _check_attn, _check_sample, _norm_case, _sample, _slopes
 
 pytestmark = pytest.mark.gpu
 
@@ -221,3 +221,31 @@ def test_qk_norm_rope_of_many_rows():
                                  ks[b:b + 1], kl[b:b + 1], depth[b:b + 1], eps=1e-5, rope_theta=5e5, rotary_dim=R)
         for a, c in zip(got, want):
             assert torch.equal(a, c)
+
+
+# ----------------------------------------------------------------------------- the weights' normaliser
+
+@pytest.mark.parametrize("B,M,Hq,Hkv,D,lens,window", [
+    (3, 3, 8, 2, 64, [40, 1, 9], 1),            # few rows, one key to a row
+    (2, 40, 16, 2, 128, [300, 77], 1),          # paired tiles, one key to a row
+    (4, 0, 4, 4, 128, [0, 1, 2, 3], 0),         # one to four keys
+    (2, 20, 12, 2, 64, [3, 30], 0),
+    (2, 0, 8, 1, 128, [5000, 70], 0),           # cut between CTAs
+])
+@pytest.mark.parametrize("softcap,bias", [(0.0, False), (20.0, False), (50.0, False), (70.0, False), (0.0, True),
+                                          (30.0, True)])
+def test_attention_scored_of_equal_values_is_that_value(B, M, Hq, Hkv, D, lens, window, softcap, bias):
+    """Every row is a mean of the V rows it reads: with one V row, or equal ones, it is exactly that row.
+
+    The products with the rounded weights are exact, and the fp32 sums of n <= 5001 of them and the normaliser's
+    reciprocal are off by less than n 2^-24 + 2^-22 < 2^-11, which does not reach the half step 2^-9 of a bf16 value."""
+    q, k, v, ks, kl, par = _attn_case(B, M, Hq, Hkv, D, lens, 61)
+    if not window:
+        for b in range(B):
+            c0, end = int(ks[b]), int(ks[b] + kl[b]) + M + 1
+            v[b, :, c0:end] = v[b, :, c0:c0 + 1].clone()
+    out, _ = _attend(q, k, v, ks, kl, par, softcap=softcap, window=window, slopes=_slopes(Hq) if bias else None)
+    for b in range(B):
+        c0 = int(ks[b] + kl[b])
+        want = v[b, :, c0:c0 + M + 1].transpose(0, 1).repeat_interleave(Hq // Hkv, 1)  # the row's own key
+        assert torch.equal(out[b], want)

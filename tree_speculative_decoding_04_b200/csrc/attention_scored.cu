@@ -229,6 +229,14 @@ __device__ __forceinline__ bool any_of_softmax(bool mine) {
   return any != 0;
 }
 
+// The tensor core takes the weights in bf16, and a row's sum takes them as they are after
+// that rounding: the output is then a mean of the V rows whatever the weights' scale (a
+// reference far from the maximum rounds the largest weight too, and with the sum of the
+// unrounded ones a row of one key would be up to 2^-8 off that key's V).
+__device__ __forceinline__ uint64_t weights_of(uint32_t pk) {
+  return f2_pack(__uint_as_float(pk << 16), __uint_as_float(pk & 0xffff0000u));
+}
+
 // One capped score (log2) from the raw product x.
 __device__ __forceinline__ float cap_score(float x, const ScoredParams& p) {
   const float t = x * x;
@@ -818,9 +826,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 8; ++e) {
                 float a0 = __uint_as_float(x[c][2 * e]), a1 = __uint_as_float(x[c][2 * e + 1]);
                 if (!BIAS) exponents(c, e, 0.f, sub2, a0, a1);
-                const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
-                l2[e & 1] = f2_add(l2[e & 1], f2_pack(p0, p1));
-                pk[c][e] = pack_bf16x2(p0, p1);  // the tensor core takes the weights in bf16
+                pk[c][e] = pack_bf16x2(fast_exp2(a0), fast_exp2(a1));
+                l2[e & 1] = f2_add(l2[e & 1], weights_of(pk[c][e]));
               }
             if (!wait_pv()) {
               to = true;
@@ -930,9 +937,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t pk[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float p0 = fast_exp2(x[2 * e]), p1 = fast_exp2(x[2 * e + 1]);
-              l2[e & 1] = f2_add(l2[e & 1], f2_pack(p0, p1));
-              pk[e] = pack_bf16x2(p0, p1);
+              pk[e] = pack_bf16x2(fast_exp2(x[2 * e]), fast_exp2(x[2 * e + 1]));
+              l2[e & 1] = f2_add(l2[e & 1], weights_of(pk[e]));
             }
             tmem_st8(t_p + c * 8, pk);
           }
