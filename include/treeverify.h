@@ -225,9 +225,9 @@ tv_status tree_attention_noalloc(const uint16_t* q, const uint16_t* k, const uin
  *   everything else as for tree_attention, head dims 64 and 128 alike; a row
  *   without a key gets zeros.  After a wait that ran out (TV_SEQ_TIMEOUT) every
  *   row of the sequence is either zero or complete.
- * Contract: the K/V rows that some query row of the sequence may read hold
- * finite values; prefix columns before the root's window are not used, whatever
- * they hold.
+ * Contract: the K/V rows of a sequence from the root's window on, all M+1 tree
+ * rows among them, hold finite values; prefix columns before it are not used,
+ * whatever they hold.
  * TV_ERR_UNSUPPORTED: B > 4096, (Hq / Hkv) * (M + 1) >= 2^21, scale > 10^4 softcap,
  * more than 2^30 tiles: B * Hkv * ceil((Hq / Hkv) (M + 1) / 128) * ceil(K / 64) with
  * K = S_cap or, if less, window + M.
@@ -311,9 +311,11 @@ tv_status tree_accept_lm_head(const uint16_t* hidden, const uint16_t* w_lm, cons
  *   min-p   of these, each token with w >= min_p[b] (off for min_p <= 0)
  * and always the first token.  Drawn is the first kept token in vocabulary
  * order whose inclusive sum of kept weights exceeds uniform[b][u] times the sum
- * of all kept weights (the last kept one if none does).  T <= 0 draws the first
- * token of the order (greedy).  A setting that is NaN counts as off (greedy for
- * the temperature).
+ * of all kept weights (the last kept one if none does); a weight below 2^-1000
+ * counts as 0, which is never drawn.  T <= 0 draws the first token of the order
+ * (greedy).  A setting that is NaN counts as off (greedy for the temperature).
+ * Weights and the sums for the draw are doubles; top-p's border is found with
+ * weights rounded to multiples of 2^-46 (V > 2^17: 2^-45).
  *
  *   logits     fp32 or bf16 [B][M+1][V], rows logits_stride elements apart
  *              (logits_stride >= V; no alignment beyond the type's own)
@@ -427,7 +429,8 @@ tv_status tree_kv_write(uint16_t* const* k_layers, uint16_t* const* v_layers, co
  *   q_weight, k_weight  bf16 [D] in, each may be NULL (no weight): element d of
  *             a normalised head is scaled by weight_offset + weight[d]
  *             (weight_offset = 0, or 1 for weights stored around zero)
- *   eps >= 0  y = x / sqrt(mean(x^2) + eps)
+ *   eps >= 0  y = x / sqrt(mean(x^2) + eps); the sum of squares is fp32, so
+ *             elements are to stay below 2^60 in magnitude
  *   q_out     bf16 [B][M+1][Hq][D] out
  *   k, v      bf16 [B][Hkv][S_cap][D] (one layer), written at columns kv_start[b]
  *             + kv_len[b] + r, r = 0..M; every other cell is left as it was
@@ -459,11 +462,12 @@ int tv_version(void);
 
 /*
  * tv_set_wait_limit_ns -- testing hook for the timeout path of tree_attention
- * (the pages have no counterpart).  Every device wait of the tensor-core
- * attention kernel is bounded; this sets, for the launches that follow in this
- * process, the limit of the pipeline waits (a stage that waits for the previous
- * one: scores, probabilities, output, K/V tiles).  A wait that runs out makes
- * the kernel give up on that sequence: its rows are zero and TV_SEQ_TIMEOUT is
+ * and tree_attention_scored (the pages have no counterpart).  Every device wait
+ * of the tensor-core attention kernels is bounded; this sets, for the launches
+ * that follow in this process, the limit of the pipeline waits (a stage that
+ * waits for the previous one: scores, probabilities, output, K/V tiles).  A wait
+ * that runs out makes the kernel give up on that sequence: its rows are zero
+ * (tree_attention_scored: those that are not complete) and TV_SEQ_TIMEOUT is
  * OR-ed into its status.  The waits that drain copies and MMAs still in flight
  * before a CTA exits keep the full 1 s limit, so a short limit never leaves work
  * behind.  ns = 0 restores the default (1 s); larger values are clamped to it.

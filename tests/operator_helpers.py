@@ -64,8 +64,10 @@ def attention_ref(q, k, v, kv_start, kv_len, parent, status, scale=None, softcap
 
 # Errors of one output of the scored attention, with u = 2^-8 the largest relative
 # error of a rounding to bf16: the output itself is rounded (u |out|), and so is
-# every softmax weight (u times the weighted mean of |v|; the normaliser sums the
-# unrounded weights).  What is left are errors of the fp32 scores: a score of size
+# every softmax weight (u times the weighted mean of |v|; as the normaliser sums the
+# rounded weights, a single output may reach u times the weighted mean of |v - out|
+# instead, for a row of few keys whose heaviest has the smallest v: up to |out| more,
+# which none of the tests' inputs comes to).  What is left are errors of the fp32 scores: a score of size
 # |s| <= 100 off by a few fp32 roundings of itself and of the sum of |q k| terms
 # (100 * 2^-20 < 2^-13 in the exponent), and the exponential's 2^-22: together
 # below 2^-12 of the weighted mean.

@@ -38,7 +38,7 @@
 // warps (kFewRows).
 // What bounds it: the softmax warps, two to a scheduler, 1.3-1.45 us per pair of tiles
 // (tensor pipe 42 %, MUFU 39 %).  Four to a scheduler, each with half of a row's
-// columns, took 616 us: twice the TMEM accesses at half the width.  (510 us now, 680
+// columns, took 616 us: twice the TMEM accesses at half the width.  (517 us now, 670
 // TFLOP/s, 0.40 of a plain bf16 GEMM's rate; a window of 4096 keys for 6 x 4 rows x 8 heads x 8
 // sequences, 135 MB, 36.7 us: 3.7 TB/s with 5 us before the first tile and 6 us of
 // epilogue and merge.)
@@ -147,7 +147,7 @@ __device__ __forceinline__ Geo sequence(const ScoredParams& p, int b) {
 // us, 14 sequences (52, 39) 55.6 / 57.2 us, 8 sequences (26, 22) 37.5 / 42.3 us; biases, 3
 // query tiles, 8 sequences (52, 33) 59.0 / 54.4 us.  Equal ranges of every sequence dealt
 // in turn took 172 us for 32 sequences with biases that take 137 us so, and 563 us for
-// 129 query rows x 64 heads x 8 sequences that take 510 us.
+// 129 query rows x 64 heads x 8 sequences that took 510 us so.
 __device__ __forceinline__ int tiles_of(int nt) { return max(nt, 1); }  // (a sequence without keys has rows to zero)
 
 struct Shares {  // (the host has checked that all of it fits in 31 bits)

@@ -41,13 +41,13 @@
 // sums run in a fixed order, so results do not depend on the order of the work.
 //
 // What bounds it.  16 x 129 rows of 128256 fp32 logits (1059 MB, 164 us at the copy rate)
-// take 250 us with min-p and 300 us with top-k (one pass, 4 TB/s and the finish), 409 us
-// at a plain temperature and 1056 us with top-p.  The pass that weighs every token is bound
+// take 248 us with min-p and 297 us with top-k (one pass, 4 TB/s and the finish), 403 us
+// at a plain temperature and 1050 us with top-p.  The pass that weighs every token is bound
 // by instruction issue (65 %: 29 instructions a token, a double exponential among them;
-// 2.5 TB/s), border by that and by the settling of its rows (144 us per 516 rows; stream
-// 105, finish 16, weigh 57).  Weighing only the sure tokens there, moved together first,
+// 2.6 TB/s), border by that and by the settling of its rows (147 us per 516 rows; stream
+// 104, finish 16, weigh 56).  Weighing only the sure tokens there, moved together first,
 // was no faster (1077 us).  A few rows are bound by launches and block-wide steps: 8 rows
-// of 151936 take 14 us with min-p, 17 at a plain temperature, 22 with top-k and 47 with a
+// of 151936 take 14 us with min-p, 17 at a plain temperature, 22 with top-k and 48 with a
 // top-p that keeps too many tokens for the finish.
 #include <algorithm>
 #include <climits>
